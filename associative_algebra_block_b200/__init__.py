@@ -40,10 +40,14 @@ EXPORTS = ("aal_project_fwd", "aal_swiglu_fwd", "aal_project_bwd", "aal_decode_m
            "aal_swiglu_decode", "aal_swiglu_bwd", "aal_square_product", "aal_block_table", "aal_block_product_count",
            "aal_get_device_status", "aal_status_string", "aal_set_path_policy",
            "aal_last_path", "aal_launch_count", "aal_version", "aal_set_timing_events",
-           "aal_swiglu_decode_noalloc", "aal_workspace_size", "aal_set_workspace")
+           "aal_swiglu_decode_noalloc", "aal_workspace_size", "aal_set_workspace",
+           "aal_layer_norm_fwd", "aal_layer_norm_bwd", "aal_layer_norm_bwd_workspace_size",
+           "aal_moe_decode")
 AAL_KERNEL_PROJECT, AAL_KERNEL_GATE_UP, AAL_KERNEL_BWD_DX = 1, 2, 3
 AAL_KERNEL_BWD_DW, AAL_KERNEL_SQUARE, AAL_KERNEL_DECODE = 4, 5, 6
 AAL_KERNEL_DECODE_GATE_UP, AAL_KERNEL_SWIGLU_BWD, AAL_KERNEL_FFN_DECODE = 7, 8, 9
+AAL_KERNEL_NORM_FWD, AAL_KERNEL_NORM_BWD = 10, 11
+AAL_KERNEL_MOE_ROUTER, AAL_KERNEL_MOE_UP, AAL_KERNEL_MOE_DOWN = 12, 13, 14
 
 
 class AalError(RuntimeError):
@@ -101,6 +105,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "aal_set_timing_events": ([i32, vp, vp], i32),
             "aal_workspace_size": ([i32, i32, i32, AalRowTypeRule, i64, i64, i64], i64),
             "aal_set_workspace": ([vp, ctypes.c_uint64], i32),
+            "aal_layer_norm_fwd": ([AalMat] * 4 + [ctypes.c_float] + [AalMat] * 2 + [vp, vp, vp], i32),
+            "aal_layer_norm_bwd": ([AalMat] * 2 + [vp, vp] + [AalMat] * 5 + [i32, vp], i32),
+            "aal_layer_norm_bwd_workspace_size": ([i64, i64], i64),
+            "aal_moe_decode": ([i32, i32, vp] + [AalMat] * 6 + [i32, i32, vp, vp] + [AalMat] * 2 + [vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -257,6 +265,90 @@ def aal_swiglu_decode_noalloc(law, q, positions, x, Wg, Wu, Wd, y, stream=None):
                                             positions.data_ptr() if positions.numel() else None,
                                             mat(x), mat(Wg), mat(Wu), mat(Wd), mat(y), _stream(stream)),
            "aal_swiglu_decode_noalloc")
+
+
+def _same_device(*tensors):
+    """The calls launch on the current device: every tensor that has entries
+    must be there."""
+    dev = None
+    for t in tensors:
+        if t is None or t.numel() == 0:
+            continue
+        if dev is None:
+            if not t.is_cuda:
+                raise ValueError("tensor must be on a CUDA device")
+            dev = t.device
+            if dev.index != torch.cuda.current_device():
+                raise ValueError(f"tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def _vec(t: torch.Tensor | None, what: str) -> AalMat:
+    """aal_mat view [1, d] of a contiguous 1-D parameter vector."""
+    if t is None:
+        return mat(None)
+    if t.dim() != 1:
+        raise ValueError(f"{what} must be 1-D")
+    return mat(t.unsqueeze(0))
+
+
+def _ptr(t: torch.Tensor | None, dtype: torch.dtype, n: int, what: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} entries")
+    return t.data_ptr() if n else None
+
+
+def aal_layer_norm_fwd(X, gamma, beta, Y, eps=1e-5, R=None, S=None, mean=None, rstd=None, stream=None):
+    """Y = layer norm of the rows of X (+ R) with gamma and beta [d] (either
+    may be None); S receives the rounded sum, mean and rstd [rows] (fp32) the
+    row statistics."""
+    n = X.shape[0] if X.dim() else 0
+    pm, ps = _ptr(mean, torch.float32, n, "mean"), _ptr(rstd, torch.float32, n, "rstd")
+    vg, vb = _vec(gamma, "gamma"), _vec(beta, "beta")
+    _same_device(X, gamma, beta, Y, R, S, mean, rstd)
+    _check(load().aal_layer_norm_fwd(mat(X), mat(R), vg, vb, eps, mat(S), mat(Y), pm, ps, _stream(stream)),
+           "aal_layer_norm_fwd")
+
+
+def aal_layer_norm_bwd(X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None, dR=None, accumulate=False,
+                       stream=None):
+    """Gradients of aal_layer_norm_fwd; dR is added to dX.  dgamma and dbeta
+    [d] come from the same pass when a workspace of
+    aal_layer_norm_bwd_workspace_size(rows, d) bytes is set."""
+    n = X.shape[0] if X.dim() else 0
+    pm, ps = _ptr(mean, torch.float32, n, "mean"), _ptr(rstd, torch.float32, n, "rstd")
+    vg, vdg, vdb = _vec(gamma, "gamma"), _vec(dgamma, "dgamma"), _vec(dbeta, "dbeta")
+    _same_device(X, gamma, mean, rstd, dY, dX, dgamma, dbeta, dR)
+    _check(load().aal_layer_norm_bwd(mat(X), vg, pm, ps, mat(dY), mat(dR), mat(dX), vdg, vdb, int(bool(accumulate)),
+                                     _stream(stream)), "aal_layer_norm_bwd")
+
+
+def aal_layer_norm_bwd_workspace_size(rows, cols) -> int:
+    """Bytes of device workspace aal_layer_norm_bwd uses for [rows, cols]."""
+    n = int(load().aal_layer_norm_bwd_workspace_size(int(rows), int(cols)))
+    if n < 0:
+        raise ValueError("aal_layer_norm_bwd_workspace_size: invalid arguments")
+    return n
+
+
+def aal_moe_decode(law, q, positions, x, Wr, Wg, Wu, Wd, ids, weights, h, y, R=None, renormalize=True, stream=None):
+    """One decode step of a mixture of SwiGLU experts: Wr [D, E], the experts
+    stacked by rows in Wg, Wu [E*D, F] and Wd [E*F, D]; ids (int32) and weights
+    (fp32) [B, top_k] receive the choices, h [B*top_k, F] is workspace."""
+    _index_vector(positions, torch.int64, x.shape[0], "positions", x)
+    if ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError("ids must be [entries, top_k]")
+    k = ids.shape[1]
+    pi, pw = _ptr(ids, torch.int32, x.shape[0] * k, "ids"), _ptr(weights, torch.float32, x.shape[0] * k, "weights")
+    _same_device(x, Wr, Wg, Wu, Wd, ids, weights, h, y, R)
+    _check(load().aal_moe_decode(_law(law), q, positions.data_ptr() if positions.numel() else None, mat(x), mat(Wr),
+                                 mat(Wg), mat(Wu), mat(Wd), mat(R), k, int(bool(renormalize)),
+                                 pi, pw, mat(h), mat(y), _stream(stream)), "aal_moe_decode")
 
 
 def aal_square_product(law, q, X, W, Z, stream=None):

@@ -552,7 +552,7 @@ const char* aal_status_string(int32_t status) {
 }
 
 aal_status aal_set_timing_events(int32_t kernel, void* before, void* after) {
-  if (kernel < AAL_KERNEL_PROJECT || kernel > AAL_KERNEL_FFN_DECODE) return AAL_ERR_INVALID_ARG;
+  if (kernel < AAL_KERNEL_PROJECT || kernel > AAL_KERNEL_MOE_DOWN) return AAL_ERR_INVALID_ARG;
   t_ev_before[kernel] = (cudaEvent_t)before;
   t_ev_after[kernel] = (cudaEvent_t)after;
   return AAL_OK;

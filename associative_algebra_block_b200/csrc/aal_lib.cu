@@ -7,3 +7,5 @@
 #include "aal_ffn_decode.cu"
 #include "aal_segments.cu"
 #include "aal_fixed_scratch.cu"
+#include "aal_norm.cu"
+#include "aal_moe.cu"

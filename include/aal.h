@@ -253,6 +253,90 @@ AAL_API aal_status aal_swiglu_decode_noalloc(int32_t law, int32_t q, const int64
 AAL_API aal_status aal_square_product(int32_t law, int32_t q, aal_mat X, aal_mat W,
                               aal_mat Z, void* stream);
 
+/*
+ * Layer norm of the rows of X, or of X + R (the residual stream), the norm
+ * ahead of the feed-forward block.  The pages measure the projections alone;
+ * this call and the next two stand beside them in a Transformer block.
+ *   s = x (+ r), mu = mean(s), v = mean((s - mu)^2), rstd = 1 / sqrt(v + eps)
+ *   y = (s - mu) rstd gamma + beta, all in fp32, y rounded once.
+ *   X, R, S, Y [M, d].  R may have ptr == NULL (no residual).  S receives s
+ *   rounded to the call's dtype (what the next residual add and the backward
+ *   read) and may have ptr == NULL; it needs R.  The norm itself uses the
+ *   unrounded sum.
+ *   gamma, beta [1, d] in the call's dtype or both in AAL_F32; ptr == NULL
+ *   stands for ones and zeros.
+ *   mean, rstd: device fp32 arrays of M entries, or NULL.
+ *   S and Y may be X or R themselves (same pointer and ld), not each other;
+ *   other overlaps are not allowed.  eps >= 0 and finite.
+ * Any M, d and ld.  Rows whose pointers and leading dimensions are multiples
+ * of 16 bytes, with d a multiple of 16 bytes of elements, move in 16-byte
+ * accesses; others element by element.
+ * Errors: AAL_ERR_INVALID_ARG for inconsistent shapes, S without R or a bad
+ * eps, AAL_ERR_UNSUPPORTED for mixed dtypes.
+ */
+AAL_API aal_status aal_layer_norm_fwd(aal_mat X, aal_mat R, aal_mat gamma, aal_mat beta, float eps,
+                              aal_mat S, aal_mat Y, float* mean, float* rstd, void* stream);
+
+/*
+ * Backward of aal_layer_norm_fwd.  With xh = (x - mean) rstd, g = dy gamma:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) (+ dr)
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy, in fp32.
+ *   X [M, d]: the normalised input (S of a forward with a residual); mean,
+ *   rstd: the forward's; dR: the gradient that reaches the same input through
+ *   the residual branch (ptr == NULL: none; it needs dX).
+ *   dX [M, d], dgamma and dbeta [1, d] (the call's dtype or both AAL_F32) may
+ *   have ptr == NULL (not computed).  dX is overwritten and may be X, dY or dR
+ *   itself; dgamma and dbeta are overwritten, or added to when accumulate != 0.
+ * With the workspace of aal_set_workspace (aal_layer_norm_bwd_workspace_size
+ * bytes) dX and the columns' sums come from one pass over X and dY: every CTA
+ * leaves its sums there and a second launch adds them in a fixed order.
+ * Without it dgamma and dbeta take a pass of their own, in a fixed order too.
+ * M may be 0 (dgamma and dbeta are then zero, or unchanged when accumulating).
+ */
+AAL_API aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const float* rstd,
+                              aal_mat dY, aal_mat dR, aal_mat dX, aal_mat dgamma, aal_mat dbeta,
+                              int32_t accumulate, void* stream);
+
+/* Workspace bytes aal_layer_norm_bwd uses for [rows, cols] (any dtype and
+ * alignment); -1 for negative arguments. */
+AAL_API int64_t aal_layer_norm_bwd_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * Decode step of a mixture of algebraic SwiGLU experts: the router, the
+ * chosen experts of aal_swiglu_decode's form and their weighted sum.
+ *   l = x Wr (dense, exact products summed in fp64)
+ *   e_1..e_k: the k = top_k largest logits, ties to the lower index
+ *   w_j = softmax(l)[e_j]; renormalize != 0: softmax over the chosen logits
+ *   y = (r) + sum_j w_j (silu(x * Wg_e) (.) (x * Wu_e)) * Wd_e, e = e_j,
+ * where each "*" is the row-typed product of entry b's row type positions[b]
+ * mod q.
+ *   positions: device int64 [B]; x [B, D]; Wr [D, E]; the experts stacked by
+ *   rows: Wg, Wu [E D, F] (expert e is rows e D .. e D + D - 1), Wd [E F, D];
+ *   R [B, D] (ptr == NULL: no residual).
+ *   ids: device int32 [B, k], weights: device fp32 [B, k]: the choices in
+ *   order of falling logit, overwritten.  h [B k, F]: caller's workspace,
+ *   overwritten with the activations of the choices.  y [B, D]: overwritten;
+ *   it may be R or x itself.
+ * Up to 128 entries take three chained launches.  bf16 calls with q <= 256,
+ * D / q and F / q multiples of 16 and 16-byte aligned rows run on the tensor
+ * cores (aal_last_path 3) and read each expert's weight blocks once for all
+ * entries that chose it (once per 16 entries of one expert); there a block
+ * that one entry of an expert uses also meets zeros from the expert's other
+ * entries, so weights have to be finite.  Other calls take the general path.
+ * Limits: top_k <= 32 and <= E, E <= 2048 (AAL_ERR_UNSUPPORTED above 32 and
+ * 2048, AAL_ERR_INVALID_ARG above E).
+ * An entry with a negative position is skipped: its row of y is not written,
+ * its ids are -1 and its weights 0, and the device status reports
+ * AAL_ERR_DEVICE_BOUNDS.  An entry whose logits hold a NaN has k different
+ * valid ids and NaN weights.
+ * Errors: AAL_ERR_INVALID_ARG for inconsistent shapes or a missing array,
+ * AAL_ERR_UNSUPPORTED for mixed dtypes.
+ */
+AAL_API aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* positions, aal_mat x,
+                          aal_mat Wr, aal_mat Wg, aal_mat Wu, aal_mat Wd, aal_mat R, int32_t top_k,
+                          int32_t renormalize, int32_t* ids, float* weights, aal_mat h, aal_mat y,
+                          void* stream);
+
 /* ---------------------------------------------------------------------- */
 /* Workspace for explicit and ragged row types                             */
 /* ---------------------------------------------------------------------- */
@@ -381,11 +465,16 @@ AAL_API int32_t aal_last_path(void);
  * aal_swiglu_bwd with the SiLU' chain; aal_swiglu_bwd's other launches use
  * the PROJECT, BWD_DX and BWD_DW kinds), AAL_KERNEL_FFN_DECODE (9, the
  * one-launch FFN decode kernel of aal_swiglu_decode; with more than 128
- * entries the pair brackets all of the call's launches).
+ * entries the pair brackets all of the call's launches), AAL_KERNEL_NORM_FWD
+ * (10), AAL_KERNEL_NORM_BWD (11, all launches of the call),
+ * AAL_KERNEL_MOE_ROUTER, _UP and _DOWN (12, 13, 14: the launches of
+ * aal_moe_decode, the first 128 entries' when there are more).
  */
 enum { AAL_KERNEL_PROJECT = 1, AAL_KERNEL_GATE_UP = 2, AAL_KERNEL_BWD_DX = 3,
        AAL_KERNEL_BWD_DW = 4, AAL_KERNEL_SQUARE = 5, AAL_KERNEL_DECODE = 6,
-       AAL_KERNEL_DECODE_GATE_UP = 7, AAL_KERNEL_SWIGLU_BWD = 8, AAL_KERNEL_FFN_DECODE = 9 };
+       AAL_KERNEL_DECODE_GATE_UP = 7, AAL_KERNEL_SWIGLU_BWD = 8, AAL_KERNEL_FFN_DECODE = 9, AAL_KERNEL_NORM_FWD = 10,
+       AAL_KERNEL_NORM_BWD = 11, AAL_KERNEL_MOE_ROUTER = 12, AAL_KERNEL_MOE_UP = 13,
+       AAL_KERNEL_MOE_DOWN = 14 };
 AAL_API aal_status aal_set_timing_events(int32_t kernel, void* before, void* after);
 
 /* Number of kernels launched by compute calls on this thread since the last

@@ -338,6 +338,60 @@ def swiglu_decode(law: str, q: int, positions, x, Wg, Wu, Wd):
     return H, decode(law, q, positions, H, Wd)
 
 
+def layer_norm(S, gamma=None, beta=None, eps: float = 1e-5):
+    """Layer norm of every row: (s - mean) / sqrt(var + eps) * gamma + beta
+    with the biased variance.  Returns (Y, mean, rstd) in float64."""
+    S = np.asarray(S, dtype=np.float64)
+    mean = S.mean(axis=1)
+    rstd = 1.0 / np.sqrt(((S - mean[:, None]) ** 2).mean(axis=1) + eps)
+    Y = (S - mean[:, None]) * rstd[:, None]
+    if gamma is not None:
+        Y = Y * np.asarray(gamma, dtype=np.float64)
+    if beta is not None:
+        Y = Y + np.asarray(beta, dtype=np.float64)
+    return Y, mean, rstd
+
+
+def layer_norm_bwd(S, gamma, mean, rstd, dY):
+    """Gradients of L = <dY, layer_norm(S)> with the given row statistics:
+    (dS, dgamma, dbeta) in float64."""
+    S, dY = np.asarray(S, dtype=np.float64), np.asarray(dY, dtype=np.float64)
+    rstd = np.asarray(rstd, dtype=np.float64)[:, None]
+    xhat = (S - np.asarray(mean, dtype=np.float64)[:, None]) * rstd
+    g = dY if gamma is None else dY * np.asarray(gamma, dtype=np.float64)
+    dS = rstd * (g - g.mean(axis=1, keepdims=True) - xhat * (g * xhat).mean(axis=1, keepdims=True))
+    return dS, (dY * xhat).sum(axis=0), dY.sum(axis=0)
+
+
+def route(x, Wr, top_k: int, renormalize: bool = True):
+    """Router of a mixture of experts: per row the top_k largest logits of
+    x Wr (ties: the lower index, in order of falling logit) and their softmax
+    weights, over all logits or over the chosen ones.  Returns (ids, weights)."""
+    logits = np.asarray(x, dtype=np.float64) @ np.asarray(Wr, dtype=np.float64)
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    p = np.exp(logits - logits.max(axis=1, keepdims=True))
+    w = np.take_along_axis(p, ids, axis=1)
+    return ids, w / (w if renormalize else p).sum(axis=1, keepdims=True)
+
+
+def moe_decode(law: str, q: int, positions, x, Wr, Wg, Wu, Wd, top_k: int, renormalize: bool = True, R=None):
+    """Decode step of a mixture of algebraic SwiGLU experts stacked by rows
+    (Wg, Wu [E*D, F], Wd [E*F, D]): the weighted sum of the chosen experts'
+    ``swiglu_decode`` plus R.  Returns (Y, ids, weights) in float64."""
+    x = np.asarray(x, dtype=np.float64)
+    D, E = x.shape[1], np.asarray(Wr).shape[1]
+    F = np.asarray(Wg).shape[1]
+    ids, weights = route(x, Wr, top_k, renormalize)
+    Y = np.zeros_like(x) if R is None else np.array(R, dtype=np.float64)
+    for e in range(E):
+        rows, slot = np.nonzero(ids == e)
+        if rows.size:
+            _, out = swiglu_decode(law, q, np.asarray(positions)[rows], x[rows], Wg[e * D:(e + 1) * D],
+                                   Wu[e * D:(e + 1) * D], Wd[e * F:(e + 1) * F])
+            Y[rows] += weights[rows, slot][:, None] * out
+    return Y, ids, weights
+
+
 def mac_ratio(law: str, q: int) -> float:
     """Fraction of a dense projection's MACs that one row type performs."""
     return block_product_count(law, q, True) / float(q * q)
