@@ -73,6 +73,8 @@ _lock = threading.Lock()
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libaal.so (once) and declare the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -209,8 +211,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream) -> int | None:
     if stream is None:
-        if not torch.cuda.is_available():
-            return None
+        if not torch.cuda.is_initialized():
+            return None  # no CUDA tensor and no stream exists yet: the default stream
         if _raw_stream is not None:
             return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
@@ -267,52 +269,80 @@ def aal_swiglu_decode_noalloc(law, q, positions, x, Wg, Wu, Wd, y, stream=None):
            "aal_swiglu_decode_noalloc")
 
 
-def _same_device(*tensors):
-    """The calls launch on the current device: every tensor that has entries
-    must be there."""
-    dev = None
-    for t in tensors:
-        if t is None or t.numel() == 0:
-            continue
-        if dev is None:
-            if not t.is_cuda:
+class _Args:
+    """Descriptors of one call's tensors.  The call launches on the current
+    device, so every tensor that has entries must be there.  (The same checks
+    as ``mat``, in fewer Python steps: a decode step's calls are short.)"""
+
+    __slots__ = ("dev",)
+
+    def __init__(self):
+        self.dev = None
+
+    def place(self, t):
+        dev = t.get_device()  # -1: a host tensor
+        if dev != self.dev:
+            if dev < 0:
                 raise ValueError("tensor must be on a CUDA device")
-            dev = t.device
-            if dev.index != torch.cuda.current_device():
-                raise ValueError(f"tensors are on {dev}, the current device is {torch.cuda.current_device()}")
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+            if self.dev is not None:
+                raise ValueError(f"tensors on CUDA devices {self.dev} and {dev}")
+            if dev != torch.cuda.current_device():
+                raise ValueError(f"tensors are on CUDA device {dev}, the current one is {torch.cuda.current_device()}")
+            self.dev = dev
+        return t.data_ptr()
+
+    def mat(self, t):
+        if t is None:
+            return _NO_MAT
+        code = _DTYPE_CODE.get(t.dtype)
+        if t.dim() != 2 or code is None:
+            return mat(t)  # refuses it
+        rows, cols = t.shape
+        if not rows or not cols:
+            return mat(t)
+        ld, unit = t.stride()
+        if unit != 1 and cols > 1:
+            raise ValueError("tensor must be row-major (unit column stride)")
+        if rows == 1:
+            ld = cols
+        return AalMat(self.place(t), code, rows, cols, ld if ld > cols else cols)
+
+    def vec(self, t, what):
+        """[1, d] view of a contiguous parameter vector."""
+        if t is None:
+            return _NO_MAT
+        code = _DTYPE_CODE.get(t.dtype)
+        if t.dim() != 1:
+            raise ValueError(f"{what} must be 1-D")
+        if code is None or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous, bf16 or fp32")
+        n = t.shape[0]
+        return AalMat(self.place(t) if n else None, code, 1, n, n)
+
+    def ptr(self, t, dtype, n, what):
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype}")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous with {n} entries")
+        return self.place(t) if n else None
 
 
-def _vec(t: torch.Tensor | None, what: str) -> AalMat:
-    """aal_mat view [1, d] of a contiguous 1-D parameter vector."""
-    if t is None:
-        return mat(None)
-    if t.dim() != 1:
-        raise ValueError(f"{what} must be 1-D")
-    return mat(t.unsqueeze(0))
-
-
-def _ptr(t: torch.Tensor | None, dtype: torch.dtype, n: int, what: str) -> int | None:
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with {n} entries")
-    return t.data_ptr() if n else None
+_DTYPE_CODE = {torch.bfloat16: AAL_BF16, torch.float32: AAL_F32}
+_NO_MAT = AalMat(None, AAL_BF16, 0, 0, 0)
 
 
 def aal_layer_norm_fwd(X, gamma, beta, Y, eps=1e-5, R=None, S=None, mean=None, rstd=None, stream=None):
     """Y = layer norm of the rows of X (+ R) with gamma and beta [d] (either
     may be None); S receives the rounded sum, mean and rstd [rows] (fp32) the
     row statistics."""
+    a = _Args()
     n = X.shape[0] if X.dim() else 0
-    pm, ps = _ptr(mean, torch.float32, n, "mean"), _ptr(rstd, torch.float32, n, "rstd")
-    vg, vb = _vec(gamma, "gamma"), _vec(beta, "beta")
-    _same_device(X, gamma, beta, Y, R, S, mean, rstd)
-    _check(load().aal_layer_norm_fwd(mat(X), mat(R), vg, vb, eps, mat(S), mat(Y), pm, ps, _stream(stream)),
-           "aal_layer_norm_fwd")
+    status = load().aal_layer_norm_fwd(a.mat(X), a.mat(R), a.vec(gamma, "gamma"), a.vec(beta, "beta"), eps, a.mat(S),
+                                       a.mat(Y), a.ptr(mean, torch.float32, n, "mean"),
+                                       a.ptr(rstd, torch.float32, n, "rstd"), _stream(stream))
+    _check(status, "aal_layer_norm_fwd")
 
 
 def aal_layer_norm_bwd(X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None, dR=None, accumulate=False,
@@ -320,12 +350,13 @@ def aal_layer_norm_bwd(X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=Non
     """Gradients of aal_layer_norm_fwd; dR is added to dX.  dgamma and dbeta
     [d] come from the same pass when a workspace of
     aal_layer_norm_bwd_workspace_size(rows, d) bytes is set."""
+    a = _Args()
     n = X.shape[0] if X.dim() else 0
-    pm, ps = _ptr(mean, torch.float32, n, "mean"), _ptr(rstd, torch.float32, n, "rstd")
-    vg, vdg, vdb = _vec(gamma, "gamma"), _vec(dgamma, "dgamma"), _vec(dbeta, "dbeta")
-    _same_device(X, gamma, mean, rstd, dY, dX, dgamma, dbeta, dR)
-    _check(load().aal_layer_norm_bwd(mat(X), vg, pm, ps, mat(dY), mat(dR), mat(dX), vdg, vdb, int(bool(accumulate)),
-                                     _stream(stream)), "aal_layer_norm_bwd")
+    status = load().aal_layer_norm_bwd(a.mat(X), a.vec(gamma, "gamma"), a.ptr(mean, torch.float32, n, "mean"),
+                                       a.ptr(rstd, torch.float32, n, "rstd"), a.mat(dY), a.mat(dR), a.mat(dX),
+                                       a.vec(dgamma, "dgamma"), a.vec(dbeta, "dbeta"), 1 if accumulate else 0,
+                                       _stream(stream))
+    _check(status, "aal_layer_norm_bwd")
 
 
 def aal_layer_norm_bwd_workspace_size(rows, cols) -> int:
@@ -340,15 +371,16 @@ def aal_moe_decode(law, q, positions, x, Wr, Wg, Wu, Wd, ids, weights, h, y, R=N
     """One decode step of a mixture of SwiGLU experts: Wr [D, E], the experts
     stacked by rows in Wg, Wu [E*D, F] and Wd [E*F, D]; ids (int32) and weights
     (fp32) [B, top_k] receive the choices, h [B*top_k, F] is workspace."""
-    _index_vector(positions, torch.int64, x.shape[0], "positions", x)
+    a = _Args()
     if ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError("ids must be [entries, top_k]")
-    k = ids.shape[1]
-    pi, pw = _ptr(ids, torch.int32, x.shape[0] * k, "ids"), _ptr(weights, torch.float32, x.shape[0] * k, "weights")
-    _same_device(x, Wr, Wg, Wu, Wd, ids, weights, h, y, R)
-    _check(load().aal_moe_decode(_law(law), q, positions.data_ptr() if positions.numel() else None, mat(x), mat(Wr),
-                                 mat(Wg), mat(Wu), mat(Wd), mat(R), k, int(bool(renormalize)),
-                                 pi, pw, mat(h), mat(y), _stream(stream)), "aal_moe_decode")
+    n, k = ids.shape
+    status = load().aal_moe_decode(_law(law), q, a.ptr(positions, torch.int64, n, "positions"), a.mat(x), a.mat(Wr),
+                                   a.mat(Wg), a.mat(Wu), a.mat(Wd), a.mat(R), k, 1 if renormalize else 0,
+                                   a.ptr(ids, torch.int32, n * k, "ids"),
+                                   a.ptr(weights, torch.float32, n * k, "weights"), a.mat(h), a.mat(y),
+                                   _stream(stream))
+    _check(status, "aal_moe_decode")
 
 
 def aal_square_product(law, q, X, W, Z, stream=None):
