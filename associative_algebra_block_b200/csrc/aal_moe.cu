@@ -32,10 +32,11 @@ constexpr int kChunk = 128;  // entries of one chain of launches
 
 // ------------------------------------------------------------------- router
 // A cluster of kRouterCtas CTAs takes TB entries: CTA r the input rows of
-// slice r, a thread VEC adjacent experts on every RL-th row of it.  The logits
-// are sums of exact products in fp64 (an expert chosen or not by a rounding
-// would change the whole row), added over the row lanes and the CTAs in a
-// fixed order.
+// slice r, a thread VEC adjacent experts on every RL-th row of it, all its
+// weight loads in flight before the first product.  The logits are sums of
+// exact products in fp64 (an expert chosen or not by a rounding would change
+// the whole row), added over the row lanes and the CTAs in a fixed order; CTA
+// b of the cluster then ranks entry b's.
 constexpr int kRouterCtas = 8, kRouterThreads = 256;
 
 struct RouterArgs {
@@ -50,12 +51,69 @@ struct RouterArgs {
 template <typename T>
 __device__ __forceinline__ double widen(T v) { return (double)ld_elem(&v); }
 
+// Unsigned keys in the order of the doubles; NaN lowest, -0 as +0.
+__device__ __forceinline__ unsigned long long order_key(double v) {
+  if (isnan(v)) return 0ull;
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
+  return (b >> 63) ? ~b : b | (1ull << 63);
+}
+
+// One warp ranks the logits l[0..E) of an entry and writes its k choices.
+__device__ void rank_logits(const double* l, int E, int k, int renorm, int* ids, float* wts) {
+  const int lane = threadIdx.x & 31;
+  // the lane's best of the experts lane, lane + 32, ... not yet taken
+  unsigned long long taken = 0;  // bit i: expert lane + 32 i (kMaxExperts fit)
+  unsigned long long best = 0;
+  int at = INT_MAX;
+  bool nan = false;
+  auto scan = [&] {
+    best = 0;
+    at = INT_MAX;
+    for (int e = lane, i = 0; e < E; e += 32, ++i) {
+      if ((taken >> i) & 1ull) continue;
+      const unsigned long long key = order_key(l[e]);
+      if (at == INT_MAX || key > best) { best = key; at = e; }
+    }
+  };
+  for (int e = lane; e < E; e += 32) nan |= isnan(l[e]);
+  nan = __any_sync(0xffffffffu, nan);
+  scan();
+  double mx = 0.0;
+  float sum = 0.f, mine = 0.f;  // lane j: the weight of choice j
+  for (int j = 0; j < k; ++j) {
+    // the largest key, then the lowest expert that has it
+    const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
+    const bool in_hi = (unsigned)(best >> 32) == hi;
+    const unsigned lo = __reduce_max_sync(0xffffffffu, in_hi ? (unsigned)best : 0u);
+    const int e = (int)__reduce_min_sync(0xffffffffu, in_hi && (unsigned)best == lo ? (unsigned)at : 0x7fffffffu);
+    const double v = l[e];
+    if (j == 0) mx = v;
+    const float p = nan ? NAN : expf((float)(v - mx));
+    sum += p;
+    if (lane == j) {
+      mine = p;
+      ids[j] = e;
+    }
+    if ((e & 31) == lane) {
+      taken |= 1ull << (e >> 5);
+      scan();
+    }
+  }
+  if (!renorm) {  // the softmax over every logit
+    sum = 0.f;
+    for (int e = lane; e < E; e += 32) sum += expf((float)(l[e] - mx));
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  if (lane < k) wts[lane] = mine / sum;
+}
+
 template <typename T, int VEC, int TB>
 __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThreads) k_moe_router(const RouterArgs a) {
+  constexpr int U = TB == 1 ? 8 : 4;  // weight loads in flight
   extern __shared__ double sm[];
-  double* part = sm;                        // [TB][E] this CTA's sums
-  double* red = part + (size_t)TB * a.E;    // [threads][VEC] (one entry at a time)
-  double* logit = red + kRouterThreads * VEC;  // [TB][E] (rank 0)
+  double* part = sm;                                 // [TB][E] this CTA's sums
+  double* red = part + (size_t)TB * a.E;             // [TB][VEC][threads]
+  double* xs = red + (size_t)TB * VEC * kRouterThreads;  // [TB][slice]
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = threadIdx.x;
   pdl_release();
@@ -63,131 +121,95 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
   const int b0 = (int)(blockIdx.x / kRouterCtas) * TB;
   const int nb = min(TB, a.B - b0);
   const int ds = (a.D + kRouterCtas - 1) / kRouterCtas;
-  const int d0 = min(a.D, rank * ds), d1 = min(a.D, d0 + ds);
+  const int d0 = min(a.D, rank * ds), nd = min(a.D, d0 + ds) - d0;
   const int ncv = (a.E + VEC - 1) / VEC;
   int cvb = 1;  // column vectors a pass
   while (cvb < ncv && cvb < kRouterThreads) cvb <<= 1;
   const int rl = kRouterThreads / cvb;  // row lanes
-  const T *x = (const T*)a.x, *wr = (const T*)a.wr;
+  const T *x = (const T*)a.x, *wr = (const T*)a.wr + (long long)d0 * a.ldr;
   for (int c0 = 0; c0 < ncv; c0 += cvb) {
     const int cv = c0 + tid % cvb, lane_r = tid / cvb;
+    const bool on = cv < ncv;
     double acc[TB][VEC];
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[b][j] = 0.0;
-    if (cv < ncv) {
-#pragma unroll 4
-      for (int d = d0 + lane_r; d < d1; d += rl) {
-        T w[VEC];
+    for (int r0 = lane_r; r0 < nd || r0 == lane_r; r0 += U * rl) {
+      T w[U][VEC];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + i * rl;
         if constexpr (VEC == 1) {
-          w[0] = wr[(long long)d * a.ldr + cv];
+          w[i][0] = on && r < nd ? wr[(long long)r * a.ldr + cv] : T(0.f);
         } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(wr + (long long)d * a.ldr + (long long)cv * VEC);
-          memcpy(w, &u, 16);
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (on && r < nd) u = __ldg(reinterpret_cast<const uint4*>(wr + (long long)r * a.ldr + (long long)cv * VEC));
+          memcpy(w[i], &u, 16);
         }
-        double xv[TB];
+      }
+      if (c0 == 0 && r0 == lane_r) {
+        // the entries' inputs, widened once, while the first weights are on their way
+        for (int i = tid; i < TB * nd; i += kRouterThreads) {
+          const int b = i / nd, r = i - b * nd;
+          xs[(size_t)b * ds + r] = b < nb ? widen(x[(long long)(b0 + b) * a.ldx + d0 + r]) : 0.0;
+        }
+        __syncthreads();
+      }
 #pragma unroll
-        for (int b = 0; b < TB; ++b) xv[b] = b < nb ? widen(x[(long long)(b0 + b) * a.ldx + d]) : 0.0;
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + i * rl;
+        if (r >= nd) break;
+        double wv[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const double wv = widen(w[j]);
+        for (int j = 0; j < VEC; ++j) wv[j] = widen(w[i][j]);
 #pragma unroll
-          for (int b = 0; b < TB; ++b) acc[b][j] = fma(wv, xv[b], acc[b][j]);
+        for (int b = 0; b < TB; ++b) {
+          const double xv = xs[(size_t)b * ds + r];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) acc[b][j] = fma(wv[j], xv, acc[b][j]);
         }
       }
     }
-    for (int b = 0; b < TB; ++b) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) red[j * kRouterThreads + tid] = 0.0;
+    for (int b = 0; b < TB; ++b)
 #pragma unroll
-      for (int bb = 0; bb < TB; ++bb)
-        if (bb == b) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) red[j * kRouterThreads + tid] = acc[bb][j];
-        }
-      __syncthreads();
-      for (int i = tid; i < cvb * VEC; i += kRouterThreads) {
-        const int j = i / cvb, c = i - j * cvb, e = (c0 + c) * VEC + j;
-        if (e < a.E) {
-          double s = 0.0;
-          for (int l = 0; l < rl; ++l) s += red[j * kRouterThreads + l * cvb + c];
-          part[(size_t)b * a.E + e] = s;
-        }
+      for (int j = 0; j < VEC; ++j) red[(size_t)(b * VEC + j) * kRouterThreads + tid] = acc[b][j];
+    __syncthreads();
+    for (int i = tid; i < TB * VEC * cvb; i += kRouterThreads) {
+      const int bj = i / cvb, c = i - bj * cvb, e = (c0 + c) * VEC + bj % VEC;
+      if (e < a.E) {
+        double s = 0.0;
+        for (int l = 0; l < rl; ++l) s += red[(size_t)bj * kRouterThreads + l * cvb + c];
+        part[(size_t)(bj / VEC) * a.E + e] = s;
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
   cl.sync();
-  if (rank == 0) {
-    for (int i = tid; i < nb * a.E; i += kRouterThreads) {
+  double* logit = red;  // this CTA's entry
+  if (rank < nb) {
+    for (int e = tid; e < a.E; e += kRouterThreads) {
       double s = 0.0;
 #pragma unroll
-      for (int r = 0; r < kRouterCtas; ++r) s += cl.map_shared_rank(part, r)[i];
-      logit[i] = s;
+      for (int r = 0; r < kRouterCtas; ++r) s += cl.map_shared_rank(part, r)[(size_t)rank * a.E + e];
+      logit[e] = s;
     }
   }
   cl.sync();  // the peers' sums have been read
-  if (rank != 0) return;
-  const int warp = tid >> 5, lane = tid & 31;
-  if (warp >= nb) return;
-  const int b = b0 + warp;
-  double* l = logit + (size_t)warp * a.E;
+  if (rank >= nb || tid >= 32) return;
+  const int b = b0 + rank;
   int* ids = a.ids + (long long)b * a.k;
   float* wts = a.weights + (long long)b * a.k;
   if (a.positions[b] < 0) {  // skipped: no expert, no output row
-    if (lane == 0) flag_device_error(kDevBounds);
-    for (int j = lane; j < a.k; j += 32) {
-      ids[j] = -1;
-      wts[j] = 0.f;
+    if (tid == 0) flag_device_error(kDevBounds);
+    if (tid < a.k) {
+      ids[tid] = -1;
+      wts[tid] = 0.f;
     }
     return;
   }
-  // the largest logit (NaN where one is NaN) and the softmax's sum
-  double mx = -INFINITY;
-  bool nan = false;
-  for (int e = lane; e < a.E; e += 32) {
-    const double v = l[e];
-    nan |= isnan(v);
-    mx = v > mx ? v : mx;
-  }
-  for (int o = 16; o > 0; o >>= 1) {
-    const double v = __shfl_xor_sync(0xffffffffu, mx, o);
-    mx = v > mx ? v : mx;
-  }
-  nan = __any_sync(0xffffffffu, nan);
-  float sum = 0.f;
-  if (!a.renorm) {
-    for (int e = lane; e < a.E; e += 32) sum += expf((float)(l[e] - mx));
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  // k rounds of the largest not yet taken; a NaN ranks as -infinity, so the
-  // chosen indices are always k different experts
-  float mine = 0.f;               // lane j: the weight of choice j
-  unsigned long long taken = 0;   // bit i: expert lane + 32 i (kMaxExperts fit)
-  for (int j = 0; j < a.k; ++j) {
-    double best = -INFINITY;
-    int at = INT_MAX;
-    for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
-      if ((taken >> i) & 1ull) continue;
-      double v = l[e];
-      if (isnan(v)) v = -INFINITY;
-      if (at == INT_MAX || v > best) { best = v; at = e; }
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v = __shfl_xor_sync(0xffffffffu, best, o);
-      const int i = __shfl_xor_sync(0xffffffffu, at, o);
-      if (i != INT_MAX && (at == INT_MAX || v > best || (v == best && i < at))) { best = v; at = i; }
-    }
-    const float p = nan ? NAN : expf((float)(best - mx));
-    if (a.renorm) sum += p;
-    if (lane == j) {
-      mine = p;
-      ids[j] = at;
-    }
-    if ((at & 31) == lane) taken |= 1ull << (at >> 5);
-  }
-  if (lane < a.k) wts[lane] = mine / sum;
+  rank_logits(logit, a.E, a.k, a.renorm, ids, wts);
 }
 
 // ------------------------------------------------- experts, tensor-core path
@@ -195,15 +217,17 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
 // mma.sync.m16n8k16: M = the columns, N = the entries, K = weight rows, 16 a
 // step.  The order of K inside a step is free as long as both operands agree,
 // so lane (g, t) = (lane / 4, lane % 4) takes rows 4t..4t+3 of the step and
-// columns 8g..8g+7: one 16-byte load a row, whole 128-byte lines a warp, and
-// the fragments of the four 16-column tiles are byte permutes of those
-// registers (tile i holds columns 8g + 2i and 8g + 2i + 1).  The weights
-// therefore go from global memory to the matrix instruction without shared
-// memory, and a warp keeps kDepth steps (kDepth * 2 KB) in flight.
-constexpr int kDepth = 4;
-constexpr int kTile = 64;       // output columns of a CTA's tile
-constexpr int kUpThreads = 256, kDownThreads = 256;
-constexpr int kMaxQ = 256;
+// columns 8g..8g+7: one 16-byte copy a row, whole 128-byte lines a warp, and
+// the fragments of the four 16-column tiles are byte permutes of those words
+// (tile i holds columns 8g + 2i and 8g + 2i + 1).  Every lane copies
+// (cp.async) exactly what it will read itself, so a warp's ring of steps needs
+// no barrier of any kind, and the ring runs on from one piece of work (an
+// expert's tile) to the next: the copies of the next piece are in flight while
+// the CTA adds up this one.
+constexpr int kTile = 64;   // output columns of a CTA's tile
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxQ = 32;   // groups of a table row fit one word
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -213,126 +237,227 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+// Copies of 16 bytes (past L1: weights are read once) and of 8 bytes; with
+// ``on`` false they fill zeros and read nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The entries (slots) of one expert, gathered by the whole CTA.
-struct Slots {
-  int n;            // slots of the expert
-  int* slot;        // [n] ascending
+struct ExpertArgs {
+  const int64_t* positions;
+  const int* ids;
+  const float* weights;
+  const __nv_bfloat16 *x, *wg, *wu, *wd, *r;
+  __nv_bfloat16 *h, *y;
+  long long ldx, ldg, ldu, ldd, ldh, ldr, ldy;
+  int law, q, B, k, E, D, F;
+  int tiles;   // column tiles of an output group
+  int passes;  // upper bound of the number of passes
+  int zsplit;  // k_moe_up: CTAs of a cluster
 };
 
-// Collects the slots s < n with ids[s] == e in ascending order into ``out``;
-// every thread returns their number.  ``cnt``: 32 ints of shared memory.
-__device__ __forceinline__ int collect(const int* ids, int n, int e, int* out, int* cnt) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int total = 0;
-  for (int s0 = 0; s0 < n; s0 += blockDim.x) {
-    const int s = s0 + (int)threadIdx.x;
-    const bool hit = s < n && ids[s] == e;
-    const unsigned m = __ballot_sync(0xffffffffu, hit);
-    if (lane == 0) cnt[warp] = __popc(m);
-    __syncthreads();
-    int before = total;
-    for (int w = 0; w < nw; ++w) {
-      const int c = cnt[w];
-      if (w < warp) before += c;
-      total += c;
-    }
-    if (hit) out[before + __popc(m & ((1u << lane) - 1u))] = s;
-    __syncthreads();
+// Up to 8 NT entries of one expert; ``types``: the row types of all of the
+// expert's entries, one bit each.
+struct Pass {
+  int expert, first, n;
+  unsigned types;
+};
+
+// What a CTA knows of the step, in dynamic shared memory.
+struct Tables {
+  Pass* pass;      // [passes]
+  int* first;      // [E] place of the expert's first entry in ``slot``
+  unsigned* tmask; // [E] row types of its entries
+  unsigned* who;   // [E][words] its entries, one bit each
+  int* slot;       // [B k] choices by expert, then by entry
+  int* type;       // [B]
+  int words;
+  __host__ __device__ static size_t bytes(int passes, int E, int B, int k) {
+    const size_t words = (B + 31) / 32;
+    return (sizeof(Pass) * passes + sizeof(int) * ((2 + words) * E + (size_t)B * k + B) + 15) / 16 * 16;
   }
-  return total;
-}
+  __device__ explicit Tables(unsigned char* p, const ExpertArgs& a) {
+    words = (a.B + 31) / 32;
+    pass = reinterpret_cast<Pass*>(p);
+    first = reinterpret_cast<int*>(pass + a.passes);
+    tmask = reinterpret_cast<unsigned*>(first + a.E);
+    who = tmask + a.E;
+    slot = reinterpret_cast<int*>(who + a.E * words);
+    type = slot + a.B * a.k;
+  }
+};
 
-// The expert of unit u.  With at least as many slots as experts a unit is an
-// expert; with fewer a unit is a slot, which stands for its expert if it is
-// the first one to choose it.  -1: the unit has no work.
-__device__ __forceinline__ int unit_expert(const int* ids, int n, int E, int u) {
-  if (n >= E) return u;
-  const int e = ids[u];
-  if (e < 0) return -1;
-  bool seen = false;
-  for (int s = threadIdx.x; s < u; s += blockDim.x) seen |= ids[s] == e;
-  return __syncthreads_or(seen) ? -1 : e;
-}
-
-// The groups that some of the n entries needs for output group kg, as a list
-// in ascending order; returns how many (every thread).
-__device__ __forceinline__ int used_groups(int law, int q, const int* types, int n, int kg, unsigned* mask,
-                                           uint16_t* list, int* count) {
-  for (int i = threadIdx.x; i < kMaxQ / 32; i += blockDim.x) mask[i] = 0u;
+// Sorts the choices by expert and entry and cuts every expert's entries into
+// passes of up to ``width``; returns the number of passes (every thread).  All
+// CTAs of a launch come to the same order: an entry chooses an expert at most
+// once, so a bit a (expert, entry) holds the choices whatever the order of
+// the atomics, and an entry's place is the number of bits below its own.
+__device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& tb, int width) {
+  __shared__ int s_passes;
+  const int n = a.B * a.k, W = tb.words;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) tb.tmask[e] = 0u;
+  for (int i = threadIdx.x; i < a.E * W; i += blockDim.x) tb.who[i] = 0u;
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const long long pos = a.positions[b];
+    tb.type[b] = pos < 0 ? 0 : (int)(pos % a.q);
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    int m[4];
-    const int c = table_members(law, q, types[i], kg, m);
-    for (int j = 0; j < c; ++j) atomicOr(&mask[m[j] >> 5], 1u << (m[j] & 31));
+  for (int s = threadIdx.x; s < n; s += blockDim.x) {
+    const int e = a.ids[s], b = s / a.k;
+    if (e >= 0) {
+      atomicOr(&tb.who[e * W + (b >> 5)], 1u << (b & 31));
+      atomicOr(&tb.tmask[e], 1u << tb.type[b]);
+    }
   }
   __syncthreads();
   if (threadIdx.x < 32) {
-    int at = 0;
-    for (int w = 0; w < kMaxQ / 32; ++w) {
-      const unsigned v = mask[w];
-      const int lane = threadIdx.x;
-      if ((v >> lane) & 1u) list[at + __popc(v & ((1u << lane) - 1u))] = (uint16_t)(w * 32 + lane);
-      at += __popc(v);
+    int base = 0, np = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + (int)threadIdx.x;
+      int c = 0;
+      if (e < a.E)
+        for (int w = 0; w < W; ++w) c += __popc(tb.who[e * W + w]);
+      const int p = (c + width - 1) / width;
+      int ci = c, pi = p;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, ci, o), v = __shfl_up_sync(0xffffffffu, pi, o);
+        if ((int)threadIdx.x >= o) {
+          ci += u;
+          pi += v;
+        }
+      }
+      const int first = base + ci - c;
+      for (int j = 0; j < p; ++j) {
+        const int done = j * width;
+        tb.pass[np + pi - p + j] = Pass{e, first + done, min(width, c - done), tb.tmask[e]};
+      }
+      if (e < a.E) tb.first[e] = first;
+      base += __shfl_sync(0xffffffffu, ci, 31);
+      np += __shfl_sync(0xffffffffu, pi, 31);
     }
-    if (threadIdx.x == 0) *count = at;
+    if (threadIdx.x == 0) s_passes = np;
   }
   __syncthreads();
-  return *count;
-}
-
-// Accumulates acc[i][nt] += (64 columns at ``w``) x (entries of the chunk) over
-// the steps first, first + stride, ... of the used groups.  ``w`` points at
-// row 0, column 8g of the tile (lanes past its width pass wide = false and
-// load nothing); xrow[nt]: the input row of entry nt * 8 + g, or null.
-template <int NT>
-__device__ __forceinline__ void stream_tile(const __nv_bfloat16* w, long long ldw, bool wide, int law, int kg,
-                                            int nused, const uint16_t* used, int gw, int first, int stride,
-                                            const __nv_bfloat16* const* xrow, const int* xtype,
-                                            float (&acc)[4][NT][4]) {
-  const int t4 = (threadIdx.x & 3) * 4;
-  const int spg = gw >> 4;  // steps a group
-  int gi = first / spg, in = first - gi * spg;
-  while (gi < nused) {
-    uint4 wv[kDepth][4];
-    uint2 xv[kDepth][NT];
-    int pg = gi, pi = in;
-#pragma unroll
-    for (int s = 0; s < kDepth; ++s) {
-      const bool on = pg < nused;
-      const int grp = on ? used[pg] : 0;
-      const long long r = (long long)grp * gw + pi * 16 + t4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        wv[s][i] = (on && wide) ? __ldg(reinterpret_cast<const uint4*>(w + (r + i) * ldw)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        xv[s][nt] = (on && xrow[nt] && in_table(law, xtype[nt], kg, grp))
-                        ? *reinterpret_cast<const uint2*>(xrow[nt] + r)
-                        : make_uint2(0, 0);
-      pi += stride;
-      while (pi >= spg) { pi -= spg; ++pg; }
-    }
-#pragma unroll
-    for (int s = 0; s < kDepth; ++s) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w0 = word(wv[s][0], i), w1 = word(wv[s][1], i), w2 = word(wv[s][2], i), w3 = word(wv[s][3], i);
-        const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-        const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(acc[i][nt], a0, a1, a2, a3, xv[s][nt].x, xv[s][nt].y);
-      }
-    }
-    gi = pg;
-    in = pi;
+  for (int s = threadIdx.x; s < n; s += blockDim.x) {
+    const int e = a.ids[s], b = s / a.k;
+    if (e < 0) continue;
+    int at = tb.first[e] + __popc(tb.who[e * W + (b >> 5)] & ((1u << (b & 31)) - 1u));
+    for (int w = 0; w < (b >> 5); ++w) at += __popc(tb.who[e * W + w]);
+    tb.slot[at] = s;
   }
+  __syncthreads();
+  return s_passes;
 }
 
-// Writes a warp's accumulators to red[n][64].
+// The input groups that output group kg needs for entries of the given types.
+__device__ __forceinline__ unsigned groups_of(int law, int q, unsigned types, int kg) {
+  if (law == AAL_LAW_Q) return types | (1u << kg);
+  unsigned m = 0;
+  for (int t = 0; t < 4; ++t)
+    if ((types >> t) & 1u)
+      for (int g = 0; g < 4; ++g)
+        if (in_table(law, t, kg, g)) m |= 1u << g;
+  return m;
+}
+
+// A warp's walk over the K steps of one piece: steps first, first + stride,
+// ... of the used groups in ascending order.
+template <int NT>
+struct Walk {
+  const __nv_bfloat16* w;        // row 0, this lane's column
+  const __nv_bfloat16* x[NT];    // input rows of entries nt * 8 + g (null: none)
+  int type[NT];
+  long long ldw;
+  unsigned left;                 // used groups from the current one on (0: the walk is over)
+  int in, spg, stride, kg;
+  bool wide;                     // this lane's columns are inside the tile
+  __device__ __forceinline__ void settle() {
+    while (in >= spg && left) {
+      in -= spg;
+      left &= left - 1u;
+    }
+  }
+  __device__ __forceinline__ void start(unsigned groups, int first) {
+    left = groups;
+    in = first;
+    settle();
+  }
+  __device__ __forceinline__ void next() {
+    in += stride;
+    settle();
+  }
+};
+// Number of steps such a walk takes.
+__device__ __forceinline__ int walk_steps(unsigned groups, int spg, int first, int stride) {
+  const int total = __popc(groups) * spg;
+  return first < total ? (total - first + stride - 1) / stride : 0;
+}
+
+template <int NT, int S>
+struct Ring {
+  static constexpr uint32_t kStep = 2048 + 256 * NT;  // bytes of one step
+  uint32_t base;  // this lane's 16-byte column of slot 0
+  uint32_t xbase;
+  int head = 0;   // slot the next step goes to
+  int tail = 0;   // slot the next product reads
+  __device__ Ring(unsigned char* mem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t p = tc::smem_u32(mem) + warp * S * kStep;
+    base = p + lane * 16;
+    xbase = p + 2048 + lane * 8;
+  }
+  // Issues the copies of the walk's step (a group of its own).
+  __device__ __forceinline__ void issue(const Walk<NT>& k, int law) {
+    const int grp = __ffs(k.left) - 1, t4 = (threadIdx.x & 3) * 4;
+    const long long r = (long long)grp * k.spg * 16 + k.in * 16 + t4;
+    const __nv_bfloat16* w = k.w + r * k.ldw;
+    const uint32_t d = base + head * kStep, dx = xbase + head * kStep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy16(d + i * 512, k.wide ? w + i * k.ldw : k.w, k.wide);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool on = k.x[nt] != nullptr && in_table(law, k.type[nt], k.kg, grp);
+      copy8(dx + nt * 256, on ? (const void*)(k.x[nt] + r) : (const void*)k.w, on);
+    }
+    head = head + 1 == S ? 0 : head + 1;
+  }
+  // The products of the oldest step.
+  __device__ __forceinline__ void multiply(float (&acc)[4][NT][4]) {
+    const uint32_t s = base + tail * kStep, sx = xbase + tail * kStep;
+    uint4 v[4];
+    uint32_t b[NT][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                   : "r"(s + i * 512)
+                   : "memory");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b[nt][0]), "=r"(b[nt][1]) : "r"(sx + nt * 256) : "memory");
+    const uint32_t w0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, w1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+    const uint32_t w2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, w3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
+      const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma16816(acc[i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+    }
+    tail = tail + 1 == S ? 0 : tail + 1;
+  }
+};
+
+// A warp's accumulators to red[8 NT][64].
 template <int NT>
 __device__ __forceinline__ void spill(float* red, const float (&acc)[4][NT][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -346,162 +471,184 @@ __device__ __forceinline__ void spill(float* red, const float (&acc)[4][NT][4]) 
     }
 }
 
-struct ExpertArgs {
-  const int64_t* positions;
-  const int* ids;
-  const float* weights;
-  const __nv_bfloat16 *x, *wg, *wu, *wd, *r;
-  __nv_bfloat16 *h, *y;
-  long long ldx, ldg, ldu, ldd, ldh, ldr, ldy;
-  int law, q, B, k, E, D, F;
-  int tiles;   // column tiles of an output group
-  int units;
-  int zsplit;  // k_moe_up: CTAs of a cluster; k_moe_down: CTAs that share an expert
-};
-
-// Lists one chunk's entries for this thread: the input rows and types of
-// entries nt * 8 + g.
-template <int NT>
-__device__ __forceinline__ void chunk_rows(const __nv_bfloat16* base, long long ld, const int* rows, const int* types,
-                                           int n0, int n, const __nv_bfloat16** xrow, int* xtype) {
-  const int g = (threadIdx.x & 31) >> 2;
+// The loop both expert kernels share: ``open(i, walk)`` describes piece i of
+// this CTA for the calling warp (false: there is none), ``steps(i)`` is that
+// warp's number of steps of it, and ``close(i)`` runs after its accumulators
+// are in red[warp] (no barrier yet).  All warps of the CTA close every piece.
+template <int NT, int S, typename Open, typename Steps, typename Close>
+__device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, int law, int pieces, Open open,
+                                           Steps steps, Close close) {
+  Ring<NT, S> ring(ring_mem);
+  Walk<NT> walk;
+  walk.left = 0;
+  int ahead = 0;  // next piece to open
+  auto produce = [&] {
+    while (!walk.left && ahead < pieces) open(ahead++, walk);
+    if (walk.left) {
+      ring.issue(walk, law);
+      walk.next();
+    }
+    copy_commit();  // empty once the work has run out, so that the waits still count
+  };
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int i = n0 + nt * 8 + g;
-    xrow[nt] = i < n ? base + (long long)rows[i] * ld : nullptr;
-    xtype[nt] = i < n ? types[i] : 0;
+  for (int i = 0; i < S - 1; ++i) produce();
+  float* mine = red + (threadIdx.x >> 5) * 8 * NT * kTile;
+  for (int i = 0; i < pieces; ++i) {
+    float acc[4][NT][4] = {};
+    for (int n = steps(i); n > 0; --n) {
+      copy_wait<S - 2>();  // the oldest step has landed
+      ring.multiply(acc);
+      produce();           // into the slot read in the round before
+    }
+    spill<NT>(mine, acc);
+    close(i);
   }
+  copy_wait<0>();
 }
 
-// h of one expert's 64 columns: warps 0-3 stream the gate's weights, warps
-// 4-7 the up projection's, each every 4 zsplit-th step; a cluster of zsplit
-// CTAs splits K further where there are few tiles and adds its parts in rank
-// order through distributed shared memory.
-template <int NT>
-__global__ void __launch_bounds__(kUpThreads, 2) k_moe_up(const ExpertArgs a) {
-  extern __shared__ float smf[];
-  __shared__ int cnt[32], nu;
-  __shared__ unsigned gmask[kMaxQ / 32];
-  __shared__ uint16_t glist[kMaxQ];
-  __shared__ int slot[kChunk], type[kChunk], tok[kChunk];
-  float* red = smf;                          // [8 warps][8 NT][64]
-  float* gu = red + 8 * 8 * NT * kTile;      // [2][8 NT][64] this CTA's gate and up sums
+// h of the passes' 64-column tiles.  A piece is (pass, tile); warps 0-3 stream
+// the gate's weights, warps 4-7 the up projection's, each every 4 zsplit-th
+// step.  The clusters (zsplit CTAs that share a piece's K range) take the
+// pieces round robin and add their parts in rank order through distributed
+// shared memory.
+template <int NT, int S>
+__global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
+  extern __shared__ __align__(128) unsigned char mem[];
+  constexpr int kRed = 8 * NT * kTile;  // floats of a warp's sums
+  unsigned char* ring_mem = mem;
+  float* red = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);
+  const Tables tb(reinterpret_cast<unsigned char*>(red + kWarps * kRed), a);
   cg::cluster_group cl = cg::this_cluster();
-  const int z = a.zsplit, rank = (int)(blockIdx.x % z), tile = (int)(blockIdx.x / z);
+  const int z = a.zsplit, rank = (int)(blockIdx.x % z), team = (int)(blockIdx.x / z), teams = (int)(gridDim.x / z);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  pdl_release();  // after the wait: a dependent that starts now finds the router's results complete
-  const int nslots = a.B * a.k;
-  const int e = unit_expert(a.ids, nslots, a.E, (int)blockIdx.y);
-  if (e < 0) return;
-  // an expert's slots belong to different entries, so there are at most kChunk
-  const int n = collect(a.ids, nslots, e, slot, cnt);
-  if (n == 0) return;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    tok[i] = slot[i] / a.k;
-    type[i] = (int)(a.positions[tok[i]] % a.q);
-  }
-  __syncthreads();
-  const int bi = a.D / a.q, bo = a.F / a.q;
-  const int kg = tile / a.tiles, c0 = kg * bo + (tile - kg * a.tiles) * kTile;
-  const int width = min(kTile, (kg + 1) * bo - c0);
-  const int nused = used_groups(a.law, a.q, type, n, kg, gmask, glist, &nu);
-  const bool wide = 8 * (lane >> 2) < width;
-  const bool up = warp >= 4;
-  const long long ldw = up ? a.ldu : a.ldg;
-  const __nv_bfloat16* w = (up ? a.wu : a.wg) + (long long)e * a.D * ldw + c0 + 8 * (lane >> 2);
-  for (int n0 = 0; n0 < n; n0 += 8 * NT) {
-    const __nv_bfloat16* xrow[NT];
-    int xtype[NT];
-    chunk_rows<NT>(a.x, a.ldx, tok, type, n0, n, xrow, xtype);
-    float acc[4][NT][4] = {};
-    stream_tile<NT>(w, ldw, wide, a.law, kg, nused, glist, bi, rank * 4 + (warp & 3), 4 * z, xrow, xtype, acc);
-    spill<NT>(red + warp * 8 * NT * kTile, acc);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * 8 * NT * kTile; i += blockDim.x) {
-      const int m = i / (8 * NT * kTile), j = i - m * 8 * NT * kTile;
-      float s = 0.f;
+  pdl_release();
+  const int np = build_tables(a, tb, 8 * NT);
+  const int bi = a.D / a.q, bo = a.F / a.q, ntile = a.q * a.tiles;
+  const int total = np * ntile;
+  const int pieces = team < total ? (total - team + teams - 1) / teams : 0;
+  const int first = rank * 4 + (warp & 3), stride = 4 * z, spg = bi >> 4;
+  auto piece = [&](int i, int& kg, int& c0) {
+    const int id = team + i * teams, p = id / ntile, tile = id - p * ntile;
+    kg = tile / a.tiles;
+    c0 = kg * bo + (tile - kg * a.tiles) * kTile;
+    return p;
+  };
+  auto open = [&](int i, Walk<NT>& w) {
+    int kg, c0;
+    const Pass p = tb.pass[piece(i, kg, c0)];
+    const int g = lane >> 2;
+    w.wide = 8 * g < (kg + 1) * bo - c0;
+    w.ldw = warp >= 4 ? a.ldu : a.ldg;
+    w.w = (warp >= 4 ? a.wu : a.wg) + (long long)p.expert * a.D * w.ldw + c0 + (w.wide ? 8 * g : 0);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s += red[(m * 4 + v) * 8 * NT * kTile + j];
-      gu[i] = s;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = nt * 8 + g;
+      const int b = n < p.n ? tb.slot[p.first + n] / a.k : 0;
+      w.x[nt] = n < p.n ? a.x + (long long)b * a.ldx : nullptr;
+      w.type[nt] = tb.type[b];
     }
+    w.spg = spg;
+    w.stride = stride;
+    w.kg = kg;
+    w.start(groups_of(a.law, a.q, p.types, kg), first);
+  };
+  auto steps = [&](int i) {
+    int kg, c0;
+    const int p = piece(i, kg, c0);
+    return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first, stride);
+  };
+  auto close = [&](int i) {
     if (z > 1) cl.sync();
     else __syncthreads();
-    // the cluster's CTAs finish the entries n mod z == rank
-    const int nc = min(8 * NT, n - n0);
-    for (int i = threadIdx.x; i < nc * kTile; i += blockDim.x) {
-      const int m = i / kTile, c = i - m * kTile;
+    int kg, c0;
+    const Pass p = tb.pass[piece(i, kg, c0)];
+    const int width = min(kTile, (kg + 1) * bo - c0);
+    // the cluster's CTAs finish every z-th entry
+    for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
+      const int m = j / kTile, c = j - m * kTile;
       if (m % z != rank || c >= width) continue;
       float g = 0.f, u = 0.f;
       for (int v = 0; v < z; ++v) {
-        const float* p = z > 1 ? cl.map_shared_rank(gu, v) : gu;
-        g += p[i];
-        u += p[8 * NT * kTile + i];
+        const float* from = z > 1 ? cl.map_shared_rank(red, v) : red;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          g += from[w * kRed + j];
+          u += from[(w + 4) * kRed + j];
+        }
       }
-      a.h[(long long)slot[n0 + m] * a.ldh + c0 + c] = __float2bfloat16_rn(g / (1.f + expf(-g)) * u);
+      a.h[(long long)tb.slot[p.first + m] * a.ldh + c0 + c] = __float2bfloat16_rn(g / (1.f + expf(-g)) * u);
     }
     if (z > 1) cl.sync();
     else __syncthreads();
-  }
+  };
+  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close);
 }
 
-// 64 columns of y: the cluster's CTAs take the experts in turn (zsplit of
-// them share one expert's K range where there are few experts), add each
-// expert's weighted product to the CTA's sums in shared memory, and the
-// cluster adds the CTAs' sums in rank order with the residual.
+// 64 columns of y a cluster.  Its CTAs take the passes in turn (or share each
+// pass's K range where there are fewer than CTAs), add every pass's weighted
+// products to their sums in shared memory, and the cluster adds the CTAs' sums
+// in rank order with the residual.
 constexpr int kDownCtas = 8;
-template <int NT>
-__global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kDownThreads, 2) k_moe_down(const ExpertArgs a) {
-  extern __shared__ float smf[];
-  __shared__ int cnt[32], nu;
-  __shared__ unsigned gmask[kMaxQ / 32];
-  __shared__ uint16_t glist[kMaxQ];
-  __shared__ int slot[kChunk], type[kChunk];
-  float* red = smf;                       // [8 warps][8 NT][64]
-  float* ys = red + 8 * 8 * NT * kTile;   // [B][64]
+template <int NT, int S>
+__global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down(const ExpertArgs a) {
+  extern __shared__ __align__(128) unsigned char mem[];
+  constexpr int kRed = 8 * NT * kTile;
+  unsigned char* ring_mem = mem;
+  float* red = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);
+  float* ys = red + kWarps * kRed;  // [B][64]
+  const Tables tb(reinterpret_cast<unsigned char*>(ys + a.B * kTile), a);
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / kDownCtas);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < a.B * kTile; i += blockDim.x) ys[i] = 0.f;
-  pdl_wait();
-  pdl_release();
-  const int nslots = a.B * a.k;
+  for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) ys[i] = 0.f;
   const int bi = a.F / a.q, bo = a.D / a.q;
   const int kg = tile / a.tiles, c0 = kg * bo + (tile - kg * a.tiles) * kTile;
   const int width = min(kTile, (kg + 1) * bo - c0);
-  const bool wide = 8 * (lane >> 2) < width;
-  const int z = a.zsplit, lanes = kDownCtas / z;
-  for (int u = rank / z; u < a.units; u += lanes) {
-    const int e = unit_expert(a.ids, nslots, a.E, u);
-    if (e < 0) continue;
-    const int n = collect(a.ids, nslots, e, slot, cnt);
-    if (n == 0) continue;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) type[i] = (int)(a.positions[slot[i] / a.k] % a.q);
-    __syncthreads();
-    const int nused = used_groups(a.law, a.q, type, n, kg, gmask, glist, &nu);
-    const __nv_bfloat16* w = a.wd + (long long)e * a.F * a.ldd + c0 + 8 * (lane >> 2);
-    for (int n0 = 0; n0 < n; n0 += 8 * NT) {
-      const __nv_bfloat16* xrow[NT];
-      int xtype[NT];
-      chunk_rows<NT>(a.h, a.ldh, slot, type, n0, n, xrow, xtype);
-      float acc[4][NT][4] = {};
-      stream_tile<NT>(w, a.ldd, wide, a.law, kg, nused, glist, bi, (rank % z) * 8 + warp, 8 * z, xrow, xtype, acc);
-      spill<NT>(red + warp * 8 * NT * kTile, acc);
-      __syncthreads();
-      const int nc = min(8 * NT, n - n0);
-      for (int i = threadIdx.x; i < nc * kTile; i += blockDim.x) {
-        float s = 0.f;
+  pdl_wait();
+  pdl_release();
+  const int np = build_tables(a, tb, 8 * NT);
+  const int z = np >= 8 ? 1 : np >= 4 ? 2 : np >= 2 ? 4 : 8;  // CTAs that share a pass
+  const int team = rank / z, teams = kDownCtas / z;
+  const int pieces = team < np ? (np - team + teams - 1) / teams : 0;
+  const int first = rank % z * kWarps + warp, stride = kWarps * z, spg = bi >> 4;
+  auto open = [&](int i, Walk<NT>& w) {
+    const Pass p = tb.pass[team + i * teams];
+    const int g = lane >> 2;
+    w.wide = 8 * g < width;
+    w.ldw = a.ldd;
+    w.w = a.wd + (long long)p.expert * a.F * a.ldd + c0 + (w.wide ? 8 * g : 0);
 #pragma unroll
-        for (int v = 0; v < 8; ++v) s += red[v * 8 * NT * kTile + i];
-        const int sl = slot[n0 + i / kTile];
-        ys[sl / a.k * kTile + i % kTile] += a.weights[sl] * s;
-      }
-      __syncthreads();
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = nt * 8 + g;
+      const int s = n < p.n ? tb.slot[p.first + n] : 0;
+      w.x[nt] = n < p.n ? a.h + (long long)s * a.ldh : nullptr;
+      w.type[nt] = tb.type[s / a.k];
     }
-  }
+    w.spg = spg;
+    w.stride = stride;
+    w.kg = kg;
+    w.start(groups_of(a.law, a.q, p.types, kg), first);
+  };
+  auto steps = [&](int i) {
+    return walk_steps(groups_of(a.law, a.q, tb.pass[team + i * teams].types, kg), spg, first, stride);
+  };
+  auto close = [&](int i) {
+    __syncthreads();
+    const Pass p = tb.pass[team + i * teams];
+    for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += red[w * kRed + j];
+      const int sl = tb.slot[p.first + j / kTile];
+      ys[sl / a.k * kTile + j % kTile] += a.weights[sl] * s;
+    }
+    __syncthreads();
+  };
+  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close);
   cl.sync();
   // the cluster's CTAs finish the entries b mod 8 == rank
-  for (int i = threadIdx.x; i < a.B * kTile; i += blockDim.x) {
+  for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) {
     const int b = i / kTile, c = i - b * kTile;
     if (b % kDownCtas != rank || c >= width || a.positions[b] < 0) continue;
     float s = a.r ? __bfloat162float(a.r[(long long)b * a.ldr + c0 + c]) : 0.f;
@@ -634,13 +781,23 @@ static aal_status launch(void (*k)(A...), dim3 grid, int threads, size_t smem, i
 
 template <typename T, int VEC, int TB>
 static aal_status run_router(const RouterArgs& a, cudaStream_t s) {
-  const size_t smem = ((size_t)2 * TB * a.E + (size_t)kRouterThreads * VEC) * sizeof(double);
+  const size_t ds = (a.D + kRouterCtas - 1) / kRouterCtas;
+  size_t red = (size_t)TB * VEC * kRouterThreads;
+  if (red < (size_t)a.E) red = a.E;  // it holds an entry's logits afterwards
+  const size_t smem = ((size_t)TB * a.E + red + TB * ds) * sizeof(double);
+  if (smem > 200 * 1024) return AAL_ERR_UNSUPPORTED;
   return launch(k_moe_router<T, VEC, TB>, dim3((unsigned)((a.B + TB - 1) / TB * kRouterCtas)), kRouterThreads, smem, 0,
                 s, a);
 }
+// Four entries a cluster share its weight loads and conversions; one entry a
+// cluster leaves more SMs to few entries, and serves what does not fit.
 template <typename T, int VEC>
 static aal_status run_router_tb(const RouterArgs& a, cudaStream_t s) {
-  return a.B <= 16 ? run_router<T, VEC, 1>(a, s) : run_router<T, VEC, 4>(a, s);
+  if (a.B > 16) {
+    const aal_status st = run_router<T, VEC, 4>(a, s);
+    if (st != AAL_ERR_UNSUPPORTED) return st;
+  }
+  return run_router<T, VEC, 1>(a, s);
 }
 
 // The widest router the kernel holds in shared memory.
@@ -651,27 +808,35 @@ static bool vec16(const aal_mat& m) {
   return !m.ptr || (((uintptr_t)m.ptr % 16) == 0 && (m.ld * es) % 16 == 0);
 }
 
-template <int NT>
+template <int NT, int S>
 static aal_status run_experts(ExpertArgs a, cudaStream_t s) {
   const int sms = device_sms();
   const int bo = a.F / a.q, bi = a.D / a.q;
+  // every expert's last pass may be part full
+  const int slots = a.B * a.k, used = slots < a.E ? slots : a.E;
+  const int most = used + slots / (8 * NT);
+  a.passes = slots < most ? slots : most;
+  const size_t ring = (size_t)kWarps * S * Ring<NT, S>::kStep + (size_t)kWarps * 8 * NT * kTile * sizeof(float);
+  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k);
   a.tiles = (bo + kTile - 1) / kTile;
-  const int utiles = a.q * a.tiles;
-  // split K over a cluster while that fills SMs and leaves every warp a step
+  const long long pieces = (long long)a.q * a.tiles * used;
+  // Split K over a cluster where that ends sooner: the rounds that the pieces
+  // need, each 1 / z of a piece long, with two steps left for every warp.
   const int steps = (a.q < 2 ? 1 : 2) * (bi >> 4);
+  auto cost = [&](int z) { return (double)((pieces + 2 * sms / z - 1) / (2 * sms / z)) / z; };
   int z = 1;
-  while (z < 8 && (long long)utiles * a.units * z * 2 <= 2LL * sms && steps >= 8 * z) z *= 2;
+  for (int w = 2; w <= 8 && steps >= 8 * w; w *= 2)
+    if (cost(w) < 0.95 * cost(z)) z = w;
   a.zsplit = z;
+  const long long room = 2LL * sms / z, teams = pieces < room ? pieces : room;
   aal_status st = timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up<NT>, dim3((unsigned)(utiles * z), (unsigned)a.units), kUpThreads,
-                  (size_t)(8 + 2) * 8 * NT * kTile * sizeof(float), z > 1 ? z : 0, s, a);
+    return launch(k_moe_up<NT, S>, dim3((unsigned)(teams * z)), kThreads, ring + tables, z > 1 ? z : 0, s, a);
   });
   if (st != AAL_OK) return st;
   a.tiles = (bi + kTile - 1) / kTile;
-  a.zsplit = a.units >= 8 ? 1 : a.units >= 4 ? 2 : a.units >= 2 ? 4 : 8;
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch(k_moe_down<NT>, dim3((unsigned)(a.q * a.tiles * kDownCtas)), kDownThreads,
-                  ((size_t)8 * 8 * NT + a.B) * kTile * sizeof(float), 0, s, a);
+    return launch(k_moe_down<NT, S>, dim3((unsigned)(a.q * a.tiles * kDownCtas)), kThreads,
+                  ring + (size_t)a.B * kTile * sizeof(float) + tables, 0, s, a);
   });
 }
 
@@ -743,8 +908,8 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
       moe::ExpertArgs a = {positions + b0, id, wt, (const bf*)at(x, b0), (const bf*)Wg.ptr, (const bf*)Wu.ptr,
                            (const bf*)Wd.ptr, (const bf*)at(R, b0), (bf*)at(h, b0 * top_k), (bf*)at(y, b0), x.ld, Wg.ld,
                            Wu.ld, Wd.ld, h.ld, R.ld, y.ld, law, q, nb, top_k, (int)E, (int)D, (int)F, 0,
-                           (int)(nb * top_k < E ? nb * top_k : E), 0};
-      st = nb <= 8 ? moe::run_experts<1>(a, s) : moe::run_experts<2>(a, s);
+                           0, 0};
+      st = nb <= 8 ? moe::run_experts<1, 4>(a, s) : moe::run_experts<2, 3>(a, s);
     } else {
       aal_mat xs = x, Rs = R, hs = h, ys = y;
       xs.ptr = at(x, b0);

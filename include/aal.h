@@ -317,7 +317,7 @@ AAL_API int64_t aal_layer_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  *   order of falling logit, overwritten.  h [B k, F]: caller's workspace,
  *   overwritten with the activations of the choices.  y [B, D]: overwritten;
  *   it may be R or x itself.
- * Up to 128 entries take three chained launches.  bf16 calls with q <= 256,
+ * Up to 128 entries take three chained launches.  bf16 calls with q <= 32,
  * D / q and F / q multiples of 16 and 16-byte aligned rows run on the tensor
  * cores (aal_last_path 3) and read each expert's weight blocks once for all
  * entries that chose it (once per 16 entries of one expert); there a block
