@@ -216,14 +216,16 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
 // A warp multiplies 64 weight columns by up to 8 NT entries with
 // mma.sync.m16n8k16: M = the columns, N = the entries, K = weight rows, 16 a
 // step.  The order of K inside a step is free as long as both operands agree,
-// so lane (g, t) = (lane / 4, lane % 4) takes rows 4t..4t+3 of the step and
-// columns 8g..8g+7: one 16-byte copy a row, whole 128-byte lines a warp, and
-// the fragments of the four 16-column tiles are byte permutes of those words
-// (tile i holds columns 8g + 2i and 8g + 2i + 1).  Every lane copies
-// (cp.async) exactly what it will read itself, so a warp's ring of steps needs
-// no barrier of any kind, and the ring runs on from one piece of work (an
-// expert's tile) to the next: the copies of the next piece are in flight while
-// the CTA adds up this one.
+// so lane (g, t) = (lane / 4, lane % 4) multiplies rows 4t..4t+3 of the step
+// and columns 8g..8g+7: one 16-byte word a row, and the fragments of the four
+// 16-column tiles are byte permutes of those words (tile i holds columns
+// 8g + 2i and 8g + 2i + 1).  The step's 16 rows of 128 bytes come in with
+// cp.async, eight lanes a row (lanes spread over four rows asked L2 for twice
+// the sectors), at a chunk position xored with 2t so that the four rows a
+// quarter warp reads together fall into different banks.  A warp's ring of
+// steps is its own: it takes no CTA barrier and runs on from one piece of work
+// (an expert's tile) to the next, so the next piece is in flight while the CTA
+// adds up this one.
 constexpr int kTile = 64;   // output columns of a CTA's tile
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -238,12 +240,12 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Copies of 16 bytes (past L1: weights are read once) and of 8 bytes; with
-// ``on`` false they fill zeros and read nothing.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+// ``bytes`` 0 they fill zeros and read nothing.
+__device__ __forceinline__ void copy(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -259,9 +261,10 @@ struct ExpertArgs {
   __nv_bfloat16 *h, *y;
   long long ldx, ldg, ldu, ldd, ldh, ldr, ldy;
   int law, q, B, k, E, D, F;
-  int tiles;   // column tiles of an output group
-  int passes;  // upper bound of the number of passes
-  int zsplit;  // k_moe_up: CTAs of a cluster
+  int passes;        // upper bound of the number of passes
+  int zsplit;        // k_moe_up: CTAs of a cluster
+  int tiles, ntile;  // column tiles of an output group, and of all groups
+  tc::FastDiv by_tiles, by_ntile, by_k;
 };
 
 // Up to 8 NT entries of one expert; ``types``: the row types of all of the
@@ -278,11 +281,13 @@ struct Tables {
   unsigned* tmask; // [E] row types of its entries
   unsigned* who;   // [E][words] its entries, one bit each
   int* slot;       // [B k] choices by expert, then by entry
+  int* entry;      // [B k] the choices' entries
+  float* weight;   // [B k] and weights
   int* type;       // [B]
   int words;
   __host__ __device__ static size_t bytes(int passes, int E, int B, int k) {
     const size_t words = (B + 31) / 32;
-    return (sizeof(Pass) * passes + sizeof(int) * ((2 + words) * E + (size_t)B * k + B) + 15) / 16 * 16;
+    return (sizeof(Pass) * passes + sizeof(int) * ((2 + words) * E + 3 * (size_t)B * k + B) + 15) / 16 * 16;
   }
   __device__ explicit Tables(unsigned char* p, const ExpertArgs& a) {
     words = (a.B + 31) / 32;
@@ -291,7 +296,9 @@ struct Tables {
     tmask = reinterpret_cast<unsigned*>(first + a.E);
     who = tmask + a.E;
     slot = reinterpret_cast<int*>(who + a.E * words);
-    type = slot + a.B * a.k;
+    entry = slot + a.B * a.k;
+    weight = reinterpret_cast<float*>(entry + a.B * a.k);
+    type = reinterpret_cast<int*>(weight + a.B * a.k);
   }
 };
 
@@ -311,7 +318,7 @@ __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& t
   }
   __syncthreads();
   for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const int e = a.ids[s], b = s / a.k;
+    const int e = a.ids[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
     if (e >= 0) {
       atomicOr(&tb.who[e * W + (b >> 5)], 1u << (b & 31));
       atomicOr(&tb.tmask[e], 1u << tb.type[b]);
@@ -348,11 +355,13 @@ __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& t
   }
   __syncthreads();
   for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const int e = a.ids[s], b = s / a.k;
+    const int e = a.ids[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
     if (e < 0) continue;
     int at = tb.first[e] + __popc(tb.who[e * W + (b >> 5)] & ((1u << (b & 31)) - 1u));
     for (int w = 0; w < (b >> 5); ++w) at += __popc(tb.who[e * W + w]);
     tb.slot[at] = s;
+    tb.entry[at] = b;
+    tb.weight[at] = a.weights[s];
   }
   __syncthreads();
   return s_passes;
@@ -370,30 +379,48 @@ __device__ __forceinline__ unsigned groups_of(int law, int q, unsigned types, in
 }
 
 // A warp's walk over the K steps of one piece: steps first, first + stride,
-// ... of the used groups in ascending order.
+// ... of the used groups in ascending order.  Inside a group a step is a
+// constant distance from the one before.
 template <int NT>
 struct Walk {
-  const __nv_bfloat16* w;        // row 0, this lane's column
-  const __nv_bfloat16* x[NT];    // input rows of entries nt * 8 + g (null: none)
+  const __nv_bfloat16* w;      // row lane / 8, column chunk lane % 8 of K step 0
+  const __nv_bfloat16* x[NT];  // input rows of entries nt * 8 + g from element 4t on
+  bool have[NT];               // the entry exists
   int type[NT];
   long long ldw;
-  unsigned left;                 // used groups from the current one on (0: the walk is over)
+  unsigned left;               // used groups from the current one on (0: the walk is over)
   int in, spg, stride, kg;
-  bool wide;                     // this lane's columns are inside the tile
-  __device__ __forceinline__ void settle() {
+  int wsize;                   // bytes copied per word: 16, or 0 past the tile's width
+  // the current step
+  const __nv_bfloat16* at;
+  int k;
+  int xsize[NT];
+  // Moves to the group that step ``in`` falls into.
+  __device__ __forceinline__ void settle(int law) {
     while (in >= spg && left) {
       in -= spg;
       left &= left - 1u;
     }
+    if (!left) return;
+    const int grp = __ffs(left) - 1;
+    k = (grp * spg + in) * 16;
+    at = w + (long long)k * ldw;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xsize[nt] = have[nt] && in_table(law, type[nt], kg, grp) ? 8 : 0;
   }
-  __device__ __forceinline__ void start(unsigned groups, int first) {
+  __device__ __forceinline__ void start(int law, unsigned groups, int first) {
     left = groups;
     in = first;
-    settle();
+    settle(law);
   }
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ void next(int law) {
     in += stride;
-    settle();
+    if (in < spg) {
+      k += stride * 16;
+      at += (long long)(stride * 16) * ldw;
+    } else {
+      settle(law);
+    }
   }
 };
 // Number of steps such a walk takes.
@@ -405,41 +432,43 @@ __device__ __forceinline__ int walk_steps(unsigned groups, int spg, int first, i
 template <int NT, int S>
 struct Ring {
   static constexpr uint32_t kStep = 2048 + 256 * NT;  // bytes of one step
-  uint32_t base;  // this lane's 16-byte column of slot 0
-  uint32_t xbase;
-  int head = 0;   // slot the next step goes to
-  int tail = 0;   // slot the next product reads
+  uint32_t put, get;   // this lane's places in slot 0: words copied, words read
+  uint32_t xpos;       // the entries' 8 bytes, copied and read by the same lane
+  uint32_t head = 0;   // slot the next step goes to (bytes)
+  uint32_t tail = 0;   // slot the next product reads (bytes)
   __device__ Ring(unsigned char* mem) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t p = tc::smem_u32(mem) + warp * S * kStep;
-    base = p + lane * 16;
-    xbase = p + 2048 + lane * 8;
+    const int g = lane >> 2, t = lane & 3;
+    put = p + (lane >> 3) * 128;  // row lane / 8 of each four; the chunk's xor depends on the row
+    get = p + t * 512 + ((g ^ (2 * t)) << 4);
+    xpos = p + 2048 + lane * 8;
   }
   // Issues the copies of the walk's step (a group of its own).
-  __device__ __forceinline__ void issue(const Walk<NT>& k, int law) {
-    const int grp = __ffs(k.left) - 1, t4 = (threadIdx.x & 3) * 4;
-    const long long r = (long long)grp * k.spg * 16 + k.in * 16 + t4;
-    const __nv_bfloat16* w = k.w + r * k.ldw;
-    const uint32_t d = base + head * kStep, dx = xbase + head * kStep;
+  __device__ __forceinline__ void issue(const Walk<NT>& k) {
+    const uint32_t chunk = threadIdx.x & 7;
+    const uint32_t d = put + head, dx = xpos + head;
+    const __nv_bfloat16* w = k.at;
+    const long long four = 4 * k.ldw;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) copy16(d + i * 512, k.wide ? w + i * k.ldw : k.w, k.wide);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const bool on = k.x[nt] != nullptr && in_table(law, k.type[nt], k.kg, grp);
-      copy8(dx + nt * 256, on ? (const void*)(k.x[nt] + r) : (const void*)k.w, on);
+    for (int i = 0; i < 4; ++i) {  // rows 4i .. 4i + 3
+      copy(d + i * 512 + ((chunk ^ (2 * i)) << 4), w, k.wsize);
+      w += four;
     }
-    head = head + 1 == S ? 0 : head + 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) copy8(dx + nt * 256, k.x[nt] + k.k, k.xsize[nt]);
+    head = head + kStep == S * kStep ? 0 : head + kStep;
   }
   // The products of the oldest step.
   __device__ __forceinline__ void multiply(float (&acc)[4][NT][4]) {
-    const uint32_t s = base + tail * kStep, sx = xbase + tail * kStep;
+    const uint32_t s = get + tail, sx = xpos + tail;
     uint4 v[4];
     uint32_t b[NT][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                   : "r"(s + i * 512)
+                   : "r"(s + i * 128)
                    : "memory");
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -453,28 +482,36 @@ struct Ring {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma16816(acc[i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
     }
-    tail = tail + 1 == S ? 0 : tail + 1;
+    tail = tail + kStep == S * kStep ? 0 : tail + kStep;
   }
 };
 
-// A warp's accumulators to red[8 NT][64].
+// A warp's sums of up to 8 NT entries by 64 columns in shared memory.  Even
+// entries come first and rows are 66 floats apart, so the fragments' stores
+// meet no bank twice.
 template <int NT>
-__device__ __forceinline__ void spill(float* red, const float (&acc)[4][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+struct Sums {
+  static constexpr int kRow = kTile + 2, kFloats = 8 * NT * kRow;
+  __device__ static __forceinline__ int at(int entry, int col) {
+    return ((entry >> 1) + (entry & 1) * 4 * NT) * kRow + col;
+  }
+  __device__ static __forceinline__ void put(float* red, const float (&acc)[4][NT][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float* p = red + (size_t)(nt * 8 + 2 * t) * kTile + 8 * g + 2 * i;
-      *reinterpret_cast<float2*>(p) = make_float2(acc[i][nt][0], acc[i][nt][2]);
-      *reinterpret_cast<float2*>(p + kTile) = make_float2(acc[i][nt][1], acc[i][nt][3]);
-    }
-}
+      for (int i = 0; i < 4; ++i) {
+        const int n = nt * 8 + 2 * t, c = 8 * g + 2 * i;
+        *reinterpret_cast<float2*>(red + at(n, c)) = make_float2(acc[i][nt][0], acc[i][nt][2]);
+        *reinterpret_cast<float2*>(red + at(n + 1, c)) = make_float2(acc[i][nt][1], acc[i][nt][3]);
+      }
+  }
+};
 
 // The loop both expert kernels share: ``open(i, walk)`` describes piece i of
-// this CTA for the calling warp (false: there is none), ``steps(i)`` is that
-// warp's number of steps of it, and ``close(i)`` runs after its accumulators
-// are in red[warp] (no barrier yet).  All warps of the CTA close every piece.
+// this CTA for the calling warp, ``steps(i)`` is that warp's number of steps of
+// it, and ``close(i)`` runs after its sums are in red[warp] (no barrier yet).
+// All warps of the CTA close every piece.
 template <int NT, int S, typename Open, typename Steps, typename Close>
 __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, int law, int pieces, Open open,
                                            Steps steps, Close close) {
@@ -485,115 +522,128 @@ __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, 
   auto produce = [&] {
     while (!walk.left && ahead < pieces) open(ahead++, walk);
     if (walk.left) {
-      ring.issue(walk, law);
-      walk.next();
+      ring.issue(walk);
+      walk.next(law);
     }
     copy_commit();  // empty once the work has run out, so that the waits still count
   };
-#pragma unroll
   for (int i = 0; i < S - 1; ++i) produce();
-  float* mine = red + (threadIdx.x >> 5) * 8 * NT * kTile;
+  float* mine = red + (threadIdx.x >> 5) * Sums<NT>::kFloats;
   for (int i = 0; i < pieces; ++i) {
     float acc[4][NT][4] = {};
     for (int n = steps(i); n > 0; --n) {
-      copy_wait<S - 2>();  // the oldest step has landed
+      copy_wait<S - 2>();  // the oldest step's copies of this lane have landed,
+      __syncwarp();        // and so have the others'; nor does any still read the slot before it
       ring.multiply(acc);
       produce();           // into the slot read in the round before
     }
-    spill<NT>(mine, acc);
+    Sums<NT>::put(mine, acc);
     close(i);
   }
   copy_wait<0>();
 }
 
 // h of the passes' 64-column tiles.  A piece is (pass, tile); warps 0-3 stream
-// the gate's weights, warps 4-7 the up projection's, each every 4 zsplit-th
-// step.  The clusters (zsplit CTAs that share a piece's K range) take the
-// pieces round robin and add their parts in rank order through distributed
-// shared memory.
+// the gate's weights, warps 4-7 the up projection's, every fourth step each.
+// The CTAs take whole pieces as long as there is one for every CTA; what is
+// left is shared by clusters of zsplit CTAs, which split K further and add
+// their parts in rank order through distributed shared memory (a last round
+// of whole pieces would leave most SMs idle).
 template <int NT, int S>
 __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
   extern __shared__ __align__(128) unsigned char mem[];
-  constexpr int kRed = 8 * NT * kTile;  // floats of a warp's sums
+  constexpr int kRed = Sums<NT>::kFloats;
   unsigned char* ring_mem = mem;
   float* red = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);
   const Tables tb(reinterpret_cast<unsigned char*>(red + kWarps * kRed), a);
   cg::cluster_group cl = cg::this_cluster();
-  const int z = a.zsplit, rank = (int)(blockIdx.x % z), team = (int)(blockIdx.x / z), teams = (int)(gridDim.x / z);
+  const int z = a.zsplit, rank = (int)(blockIdx.x % z);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_release();
   const int np = build_tables(a, tb, 8 * NT);
-  const int bi = a.D / a.q, bo = a.F / a.q, ntile = a.q * a.tiles;
-  const int total = np * ntile;
-  const int pieces = team < total ? (total - team + teams - 1) / teams : 0;
-  const int first = rank * 4 + (warp & 3), stride = 4 * z, spg = bi >> 4;
+  const int bi = a.D / a.q, bo = a.F / a.q, spg = bi >> 4;
+  const int total = np * a.ntile;
+  const int whole = z > 1 ? total / (int)gridDim.x : (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int team = (int)(blockIdx.x / z), teams = (int)(gridDim.x / z);
+  const int rest = z > 1 ? total - whole * (int)gridDim.x - team : 0;  // pieces left from this cluster's first on
+  const int pieces = whole + (rest > 0 ? (rest + teams - 1) / teams : 0);
+  // piece i: its pass, output group and first column
   auto piece = [&](int i, int& kg, int& c0) {
-    const int id = team + i * teams, p = id / ntile, tile = id - p * ntile;
-    kg = tile / a.tiles;
+    const int id = i < whole ? (int)blockIdx.x + i * (int)gridDim.x
+                             : whole * (int)gridDim.x + team + (i - whole) * teams;
+    const int p = (int)tc::fdiv((uint32_t)id, a.by_ntile), tile = id - p * a.ntile;
+    kg = (int)tc::fdiv((uint32_t)tile, a.by_tiles);
     c0 = kg * bo + (tile - kg * a.tiles) * kTile;
     return p;
   };
+  const int w4 = warp & 3;
+  auto first = [&](int i) { return i < whole ? w4 : rank * 4 + w4; };
+  auto stride = [&](int i) { return i < whole ? 4 : 4 * z; };
+  const long long ldw = warp >= 4 ? a.ldu : a.ldg;
+  const __nv_bfloat16* wbase = (warp >= 4 ? a.wu : a.wg) + (long long)(lane >> 3) * ldw;
   auto open = [&](int i, Walk<NT>& w) {
     int kg, c0;
     const Pass p = tb.pass[piece(i, kg, c0)];
-    const int g = lane >> 2;
-    w.wide = 8 * g < (kg + 1) * bo - c0;
-    w.ldw = warp >= 4 ? a.ldu : a.ldg;
-    w.w = (warp >= 4 ? a.wu : a.wg) + (long long)p.expert * a.D * w.ldw + c0 + (w.wide ? 8 * g : 0);
+    const int col = 8 * (lane & 7);
+    const bool wide = col < (kg + 1) * bo - c0;
+    w.wsize = wide ? 16 : 0;
+    w.ldw = ldw;
+    w.w = wbase + (long long)p.expert * a.D * ldw + c0 + (wide ? col : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = nt * 8 + g;
-      const int b = n < p.n ? tb.slot[p.first + n] / a.k : 0;
-      w.x[nt] = n < p.n ? a.x + (long long)b * a.ldx : nullptr;
+      const int n = nt * 8 + (lane >> 2);
+      w.have[nt] = n < p.n;
+      const int b = tb.entry[p.first + (n < p.n ? n : 0)];
+      w.x[nt] = a.x + (long long)b * a.ldx + 4 * (lane & 3);
       w.type[nt] = tb.type[b];
     }
     w.spg = spg;
-    w.stride = stride;
+    w.stride = stride(i);
     w.kg = kg;
-    w.start(groups_of(a.law, a.q, p.types, kg), first);
+    w.start(a.law, groups_of(a.law, a.q, p.types, kg), first(i));
   };
   auto steps = [&](int i) {
     int kg, c0;
     const int p = piece(i, kg, c0);
-    return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first, stride);
+    return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first(i), stride(i));
   };
   auto close = [&](int i) {
-    if (z > 1) cl.sync();
+    const bool shared = i >= whole;
+    if (shared) cl.sync();
     else __syncthreads();
     int kg, c0;
     const Pass p = tb.pass[piece(i, kg, c0)];
     const int width = min(kTile, (kg + 1) * bo - c0);
-    // the cluster's CTAs finish every z-th entry
     for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
-      const int m = j / kTile, c = j - m * kTile;
-      if (m % z != rank || c >= width) continue;
+      const int m = j / kTile, c = j % kTile, o = Sums<NT>::at(m, c);
+      if (c >= width || (shared && m % z != rank)) continue;  // a cluster's CTAs finish every z-th entry
       float g = 0.f, u = 0.f;
-      for (int v = 0; v < z; ++v) {
-        const float* from = z > 1 ? cl.map_shared_rank(red, v) : red;
+      for (int v = 0; v < (shared ? z : 1); ++v) {
+        const float* from = shared ? cl.map_shared_rank(red, v) : red;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          g += from[w * kRed + j];
-          u += from[(w + 4) * kRed + j];
+          g += from[w * kRed + o];
+          u += from[(w + 4) * kRed + o];
         }
       }
       a.h[(long long)tb.slot[p.first + m] * a.ldh + c0 + c] = __float2bfloat16_rn(g / (1.f + expf(-g)) * u);
     }
-    if (z > 1) cl.sync();
+    if (shared) cl.sync();
     else __syncthreads();
   };
   run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close);
 }
 
-// 64 columns of y a cluster.  Its CTAs take the passes in turn (or share each
-// pass's K range where there are fewer than CTAs), add every pass's weighted
-// products to their sums in shared memory, and the cluster adds the CTAs' sums
-// in rank order with the residual.
+// 64 columns of y a cluster.  Its CTAs take the passes in turn, add every
+// pass's weighted products to their sums in shared memory, and the cluster
+// adds the CTAs' sums in rank order with the residual.  The passes that are
+// left when there is no longer one for every CTA are split along K.
 constexpr int kDownCtas = 8;
 template <int NT, int S>
 __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down(const ExpertArgs a) {
   extern __shared__ __align__(128) unsigned char mem[];
-  constexpr int kRed = 8 * NT * kTile;
+  constexpr int kRed = Sums<NT>::kFloats;
   unsigned char* ring_mem = mem;
   float* red = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);
   float* ys = red + kWarps * kRed;  // [B][64]
@@ -602,46 +652,50 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
   const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / kDownCtas);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) ys[i] = 0.f;
-  const int bi = a.F / a.q, bo = a.D / a.q;
+  const int bi = a.F / a.q, bo = a.D / a.q, spg = bi >> 4;
   const int kg = tile / a.tiles, c0 = kg * bo + (tile - kg * a.tiles) * kTile;
   const int width = min(kTile, (kg + 1) * bo - c0);
   pdl_wait();
   pdl_release();
   const int np = build_tables(a, tb, 8 * NT);
-  const int z = np >= 8 ? 1 : np >= 4 ? 2 : np >= 2 ? 4 : 8;  // CTAs that share a pass
-  const int team = rank / z, teams = kDownCtas / z;
-  const int pieces = team < np ? (np - team + teams - 1) / teams : 0;
-  const int first = rank % z * kWarps + warp, stride = kWarps * z, spg = bi >> 4;
+  const int whole = np / kDownCtas, left = np - whole * kDownCtas;
+  const int z = left > 4 ? 1 : left > 2 ? 2 : left == 2 ? 4 : 8;  // CTAs that share a left-over pass
+  const int pieces = whole + (rank / z < left ? 1 : 0);
+  auto pass = [&](int i) { return i < whole ? i * kDownCtas + rank : whole * kDownCtas + rank / z; };
+  auto first = [&](int i) { return i < whole ? warp : rank % z * kWarps + warp; };
+  auto stride = [&](int i) { return i < whole ? kWarps : kWarps * z; };
+  const int col = 8 * (lane & 7);
+  const bool wide = col < width;
+  const __nv_bfloat16* wbase = a.wd + (long long)(lane >> 3) * a.ldd + c0 + (wide ? col : 0);
   auto open = [&](int i, Walk<NT>& w) {
-    const Pass p = tb.pass[team + i * teams];
-    const int g = lane >> 2;
-    w.wide = 8 * g < width;
+    const Pass p = tb.pass[pass(i)];
+    w.wsize = wide ? 16 : 0;
     w.ldw = a.ldd;
-    w.w = a.wd + (long long)p.expert * a.F * a.ldd + c0 + (w.wide ? 8 * g : 0);
+    w.w = wbase + (long long)p.expert * a.F * a.ldd;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = nt * 8 + g;
-      const int s = n < p.n ? tb.slot[p.first + n] : 0;
-      w.x[nt] = n < p.n ? a.h + (long long)s * a.ldh : nullptr;
-      w.type[nt] = tb.type[s / a.k];
+      const int n = nt * 8 + (lane >> 2), at = p.first + (n < p.n ? n : 0);
+      w.have[nt] = n < p.n;
+      w.x[nt] = a.h + (long long)tb.slot[at] * a.ldh + 4 * (lane & 3);
+      w.type[nt] = tb.type[tb.entry[at]];
     }
     w.spg = spg;
-    w.stride = stride;
+    w.stride = stride(i);
     w.kg = kg;
-    w.start(groups_of(a.law, a.q, p.types, kg), first);
+    w.start(a.law, groups_of(a.law, a.q, p.types, kg), first(i));
   };
   auto steps = [&](int i) {
-    return walk_steps(groups_of(a.law, a.q, tb.pass[team + i * teams].types, kg), spg, first, stride);
+    return walk_steps(groups_of(a.law, a.q, tb.pass[pass(i)].types, kg), spg, first(i), stride(i));
   };
   auto close = [&](int i) {
     __syncthreads();
-    const Pass p = tb.pass[team + i * teams];
+    const Pass p = tb.pass[pass(i)];
     for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
+      const int m = j / kTile, c = j % kTile, o = Sums<NT>::at(m, c);
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += red[w * kRed + j];
-      const int sl = tb.slot[p.first + j / kTile];
-      ys[sl / a.k * kTile + j % kTile] += a.weights[sl] * s;
+      for (int w = 0; w < kWarps; ++w) s += red[w * kRed + o];
+      ys[tb.entry[p.first + m] * kTile + c] += tb.weight[p.first + m] * s;
     }
     __syncthreads();
   };
@@ -649,9 +703,10 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
   cl.sync();
   // the cluster's CTAs finish the entries b mod 8 == rank
   for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) {
-    const int b = i / kTile, c = i - b * kTile;
+    const int b = i / kTile, c = i % kTile;
     if (b % kDownCtas != rank || c >= width || a.positions[b] < 0) continue;
     float s = a.r ? __bfloat162float(a.r[(long long)b * a.ldr + c0 + c]) : 0.f;
+#pragma unroll
     for (int v = 0; v < kDownCtas; ++v) s += cl.map_shared_rank(ys, v)[i];
     a.y[(long long)b * a.ldy + c0 + c] = __float2bfloat16_rn(s);
   }
@@ -809,35 +864,54 @@ static bool vec16(const aal_mat& m) {
 }
 
 template <int NT, int S>
-static aal_status run_experts(ExpertArgs a, cudaStream_t s) {
+static size_t ring_bytes() {
+  return (size_t)kWarps * (S * Ring<NT, S>::kStep + Sums<NT>::kFloats * sizeof(float));
+}
+constexpr size_t kHalfSm = 113 * 1024;  // shared memory of a CTA that leaves room for a second one
+
+template <int NT, int S>
+static aal_status run_up(ExpertArgs a, size_t tables, cudaStream_t s) {
   const int sms = device_sms();
   const int bo = a.F / a.q, bi = a.D / a.q;
+  a.tiles = (bo + kTile - 1) / kTile;
+  a.ntile = a.q * a.tiles;
+  a.by_tiles = tc::make_fastdiv((uint32_t)a.tiles);
+  a.by_ntile = tc::make_fastdiv((uint32_t)a.ntile);
+  // clusters for the pieces left over, while every warp of one keeps two steps
+  // (one step a warp: a token's 16-step pieces end no sooner)
+  const int steps = (a.q < 2 ? 1 : 2) * (bi >> 4);
+  const int z = steps >= 32 ? 4 : steps >= 16 ? 2 : 1;
+  a.zsplit = z;
+  const int used = a.B * a.k < a.E ? a.B * a.k : a.E;
+  const long long pieces = (long long)a.ntile * used * z, room = 2LL * sms / z * z;
+  return timed(AAL_KERNEL_MOE_UP, s, [&] {
+    return launch(k_moe_up<NT, S>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, ring_bytes<NT, S>() + tables,
+                  z > 1 ? z : 0, s, a);
+  });
+}
+template <int NT, int S>
+static aal_status run_down(ExpertArgs a, size_t tables, cudaStream_t s) {
+  const int bo = a.D / a.q;
+  a.tiles = (bo + kTile - 1) / kTile;
+  a.ntile = a.q * a.tiles;
+  return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
+    return launch(k_moe_down<NT, S>, dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
+                  ring_bytes<NT, S>() + (size_t)a.B * kTile * sizeof(float) + tables, 0, s, a);
+  });
+}
+// NT tiles of 8 entries a pass; a ring of four steps where two CTAs still
+// share a SM, else of three.
+template <int NT>
+static aal_status run_experts(ExpertArgs a, cudaStream_t s) {
   // every expert's last pass may be part full
   const int slots = a.B * a.k, used = slots < a.E ? slots : a.E;
   const int most = used + slots / (8 * NT);
   a.passes = slots < most ? slots : most;
-  const size_t ring = (size_t)kWarps * S * Ring<NT, S>::kStep + (size_t)kWarps * 8 * NT * kTile * sizeof(float);
-  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k);
-  a.tiles = (bo + kTile - 1) / kTile;
-  const long long pieces = (long long)a.q * a.tiles * used;
-  // Split K over a cluster where that ends sooner: the rounds that the pieces
-  // need, each 1 / z of a piece long, with two steps left for every warp.
-  const int steps = (a.q < 2 ? 1 : 2) * (bi >> 4);
-  auto cost = [&](int z) { return (double)((pieces + 2 * sms / z - 1) / (2 * sms / z)) / z; };
-  int z = 1;
-  for (int w = 2; w <= 8 && steps >= 8 * w; w *= 2)
-    if (cost(w) < 0.95 * cost(z)) z = w;
-  a.zsplit = z;
-  const long long room = 2LL * sms / z, teams = pieces < room ? pieces : room;
-  aal_status st = timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up<NT, S>, dim3((unsigned)(teams * z)), kThreads, ring + tables, z > 1 ? z : 0, s, a);
-  });
+  a.by_k = tc::make_fastdiv((uint32_t)a.k);
+  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k), sums = (size_t)a.B * kTile * sizeof(float);
+  const aal_status st = ring_bytes<NT, 4>() + tables <= kHalfSm ? run_up<NT, 4>(a, tables, s) : run_up<NT, 3>(a, tables, s);
   if (st != AAL_OK) return st;
-  a.tiles = (bi + kTile - 1) / kTile;
-  return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch(k_moe_down<NT, S>, dim3((unsigned)(a.q * a.tiles * kDownCtas)), kThreads,
-                  ring + (size_t)a.B * kTile * sizeof(float) + tables, 0, s, a);
-  });
+  return ring_bytes<NT, 4>() + tables + sums <= kHalfSm ? run_down<NT, 4>(a, tables, s) : run_down<NT, 3>(a, tables, s);
 }
 
 template <typename T>
@@ -908,8 +982,9 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
       moe::ExpertArgs a = {positions + b0, id, wt, (const bf*)at(x, b0), (const bf*)Wg.ptr, (const bf*)Wu.ptr,
                            (const bf*)Wd.ptr, (const bf*)at(R, b0), (bf*)at(h, b0 * top_k), (bf*)at(y, b0), x.ld, Wg.ld,
                            Wu.ld, Wd.ld, h.ld, R.ld, y.ld, law, q, nb, top_k, (int)E, (int)D, (int)F, 0,
-                           0, 0};
-      st = nb <= 8 ? moe::run_experts<1, 4>(a, s) : moe::run_experts<2, 3>(a, s);
+                           0, 0, 0, 0, {}, {}, {}};
+      // two tiles of entries a pass where experts get more than six on average
+      st = (long long)nb * top_k <= 6 * E ? moe::run_experts<1>(a, s) : moe::run_experts<2>(a, s);
     } else {
       aal_mat xs = x, Rs = R, hs = h, ys = y;
       xs.ptr = at(x, b0);
