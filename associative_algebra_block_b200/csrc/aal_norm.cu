@@ -18,6 +18,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace aal {
 namespace norm {
 
@@ -153,21 +155,23 @@ __device__ __forceinline__ void pdl_begin() {
 
 
 // ------------------------------------------------- rows through shared memory
-// The vector kernels bring their rows in with bulk asynchronous copies: a
-// group (the warp of a narrow row, the CTA of a wide one) owns a ring of
-// stages, each one row of every input array, and one of its threads refills a
-// stage as soon as the group is done with it, so the next rows are in flight
-// while one is reduced.  That keeps about 100 KB a SM moving with 16 warps,
-// which plain loads could not: their registers held one row a warp and nothing
-// moved during the reductions.
+// Rows come in with bulk asynchronous copies: a group (a warp for narrow rows,
+// the CTA for wide ones) owns a ring of stages, each holding its next row (or
+// rows, several narrow ones share a warp) of every input array, and one thread
+// refills a stage as soon as the group is done with it.  The next rows are so
+// in flight while one is reduced, about 100 KB a SM, which plain loads could
+// not do: their registers held one row and nothing moved during the
+// reductions.
+//
+// A bulk copy moves whole 16-byte words.  Where rows start on them (the vector
+// form) a thread takes 16-byte vectors; elsewhere (the element form) the copy
+// brings the words that lie inside the row, a few threads fetch the elements
+// before and after them (a row ahead, through registers), and a thread takes
+// elements TPR apart.
 constexpr int kMaxRing = 4;
+constexpr int kRowsPerCta = 8;  // groups of a CTA of warps
 constexpr unsigned long long kRingWaitNs = 2000000000ull;
 
-__device__ __forceinline__ void ring_init(uint64_t* bar) { tc::mbar_init(bar, 1); }
-__device__ __forceinline__ void ring_init_done() {
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  tc::fence_async_smem();
-}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
@@ -186,79 +190,275 @@ __device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// Bytes of a stage's copy of one array: ``rows`` rows of d elements, in the
+// element form with room for the row's offset from a 16-byte boundary.
+__host__ __device__ __forceinline__ uint32_t region_bytes(long long d, int es, int rows, bool elem) {
+  return elem ? (uint32_t)((d * es + 30) / 16 * 16) : (uint32_t)(d * es * rows);
+}
+
+// Where the pieces of a row lie (element form).
+struct Edges {
+  uint32_t off;         // bytes from the region's start to element 0
+  uint32_t from, size;  // the whole words inside the row: offset from element 0, bytes
+  int head, tail;       // elements before and after them
+};
+template <typename T>
+__device__ __forceinline__ Edges edges_of(const T* row, int d) {
+  const uint32_t a = (uint32_t)((uintptr_t)row & 15), len = (uint32_t)(d * sizeof(T));
+  Edges e;
+  e.off = a;
+  e.from = (16u - a) & 15u;
+  const uint32_t end = (a + len) & ~15u;  // past the last whole word, from the boundary below the row
+  if (e.from >= len || end <= a + e.from) {
+    e.from = e.size = 0;
+    e.head = d;  // no whole word: fewer than 16 bytes either side
+    e.tail = 0;
+  } else {
+    e.size = end - a - e.from;
+    e.head = (int)(e.from / sizeof(T));
+    e.tail = (int)((a + len - end) / sizeof(T));
+  }
+  return e;
+}
+constexpr int kEdgeThreads = 32;  // threads 0-15 take elements before the words, 16-31 after them
+// The element of the row's edges that thread t fetches, or -1.
+__device__ __forceinline__ int edge_index(const Edges& e, int d, int t) {
+  if (t < 16) return t < e.head ? t : -1;
+  return t - 16 < e.tail ? d - e.tail + t - 16 : -1;
+}
+
+// What a group knows of its place in the launch.
+template <int TPR, bool SUB>
+struct Group {
+  static constexpr bool BLOCK = TPR != 32;
+  int tpr, t, lane;     // threads a row, this thread's place in its row, in its group
+  int index;            // group within the CTA
+  int rpw, sub;         // rows a group takes at once, this thread's one of them
+  long long first, step;  // blocks of rpw rows
+  __device__ __forceinline__ explicit Group(int lpr) {
+    lane = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & 31);
+    index = BLOCK ? 0 : (int)(threadIdx.x >> 5);
+    tpr = SUB ? lpr : TPR ? TPR : (int)blockDim.x;
+    rpw = SUB ? 32 / lpr : 1;
+    sub = SUB ? lane / lpr : 0;
+    t = SUB ? lane % lpr : lane;
+    first = BLOCK ? (long long)blockIdx.x : (long long)blockIdx.x * kRowsPerCta + index;
+    step = BLOCK ? (long long)gridDim.x : (long long)gridDim.x * kRowsPerCta;
+  }
+  __device__ __forceinline__ void sync() const {
+    if (BLOCK) __syncthreads();
+    else __syncwarp();
+  }
+  // Sum of (a, b) over the row's threads.
+  __device__ __forceinline__ float2 sum(float a, float b, float2 (*buf)[32], int& turn) const {
+    if (BLOCK) return block_sum2(a, b, buf, turn);
+    return make_float2(sum(a), sum(b));
+  }
+  __device__ __forceinline__ float sum(float a, float2 (*buf)[32], int& turn) const {
+    return BLOCK ? block_sum2(a, 0.f, buf, turn).x : sum(a);
+  }
+  __device__ __forceinline__ float sum(float a) const {
+    if (!SUB) return warp_sum(a);
+    for (int o = tpr >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+  }
+};
+
+// Copies the rows of block rb of one array into a stage's region.
+template <typename T, bool SUB, bool ELEM>
+__device__ __forceinline__ void fill_region(uint32_t dst, const T* p, long long ld, int d, long long rb, int rpw,
+                                            int rows, uint64_t* bar) {
+  const T* src = p + rb * rpw * ld;
+  if constexpr (ELEM) {
+    const Edges e = edges_of(src, d);
+    if (e.size) bulk_load(dst + e.off + e.from, (const char*)src + e.from, e.size, bar);
+  } else if constexpr (!SUB) {
+    bulk_load(dst, src, (uint32_t)(d * sizeof(T)), bar);
+  } else if (ld == d) {
+    bulk_load(dst, src, (uint32_t)(d * sizeof(T)) * rows, bar);
+  } else {
+    for (int i = 0; i < rows; ++i)
+      bulk_load(dst + i * (uint32_t)(d * sizeof(T)), src + i * ld, (uint32_t)(d * sizeof(T)), bar);
+  }
+}
+// and how many bytes that is.
+template <typename T, bool ELEM>
+__device__ __forceinline__ uint32_t fill_bytes(const T* p, long long ld, int d, long long rb, int rpw, int rows) {
+  return ELEM ? edges_of(p + rb * rpw * ld, d).size : (uint32_t)(d * sizeof(T)) * rows;
+}
+
+// A thread's vector i of a row in shared memory (16 bytes, or that many
+// elements TPR apart), as pairs; elements past the row read as zero.
+template <typename T, bool ELEM, int TPR>
+__device__ __forceinline__ void row_get(uint32_t row, int i, int tpr, int left, f32x2 (&v)[Vec<T>::pairs]) {
+  constexpr int n = Vec<T>::n;
+  if constexpr (!ELEM) {
+    widen(lds128(row + i * tpr * 16), v, T());
+  } else {
+    float e[n];
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int k = (i * n + j) * TPR;
+      e[j] = 0.f;
+      if (k < left) {
+        if constexpr (sizeof(T) == 2) {
+          unsigned short h;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(row + k * 2));
+          e[j] = __uint_as_float((uint32_t)h << 16);
+        } else {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e[j]) : "r"(row + k * 4));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < Vec<T>::pairs; ++j) v[j] = pair(e[2 * j], e[2 * j + 1]);
+  }
+}
+template <typename T, bool ELEM, int TPR>
+__device__ __forceinline__ void row_put(T* row, int i, int tpr, int left, const f32x2 (&v)[Vec<T>::pairs]) {
+  constexpr int n = Vec<T>::n;
+  if constexpr (!ELEM) {
+    *reinterpret_cast<uint4*>(row + i * tpr * n) = narrow(v, T());
+  } else {
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int k = (i * n + j) * TPR;
+      float a, b;
+      unpair(v[j / 2], a, b);
+      if (k < left) row[k] = from_f32<T>(j & 1 ? b : a);
+    }
+  }
+}
+// A thread's part of a parameter vector in registers.
+template <typename T, typename TP, bool ELEM, int TPR>
+struct ParamPart {
+  static constexpr int n = Vec<T>::n;
+  std::conditional_t<ELEM, float[n], Param<T, TP>> u;
+  __device__ __forceinline__ void load(const TP* p, int i, int tpr, int left) {
+    if constexpr (ELEM) {
+#pragma unroll
+      for (int j = 0; j < n; ++j) u[j] = (i * n + j) * TPR < left ? as_f32(p[(i * n + j) * TPR]) : 0.f;
+    } else {
+      u.load(p + i * tpr * n);
+    }
+  }
+  __device__ __forceinline__ void get(f32x2 (&o)[Vec<T>::pairs]) const {
+    if constexpr (ELEM) {
+#pragma unroll
+      for (int j = 0; j < Vec<T>::pairs; ++j) o[j] = pair(u[2 * j], u[2 * j + 1]);
+    } else {
+      u.get(o);
+    }
+  }
+};
+
 struct FwdArgs {
   const void *x, *r, *gamma, *beta;
   void *s, *y;
   float *mean, *rstd;
   long long rows, d, ldx, ldr, lds, ldy;
   float eps;
-  int ring;  // stages of the pipelined kernels
+  int ring;  // stages
+  int lpr;   // lanes a row (warps)
 };
 
-constexpr int kRowsPerCta = 8;  // warp-per-row kernels: one row a warp
-
-// The vector kernel: NV 16-byte vectors a thread, at most MAXT threads.
-template <typename T, typename TP, int NV, bool BLOCK, int MAXT>
-__global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_fwd_ring(const FwdArgs a) {
+// TPR: 32 a warp a row (SUB: lpr lanes of one), 0 the CTA of any size, else the
+// CTA of that size.  NV vectors a thread.  MAXT, MINB: the largest CTA, and
+// how many of them a SM is to hold.
+template <typename T, typename TP, int NV, int TPR, bool SUB, bool ELEM, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
   constexpr int VEC = Vec<T>::n, P = Vec<T>::pairs;
+  constexpr bool BLOCK = TPR != 32;
   extern __shared__ __align__(128) unsigned char ring_mem[];
   __shared__ float2 buf[2][32];
   __shared__ __align__(8) uint64_t bars[(BLOCK ? 1 : kRowsPerCta) * kMaxRing];
-  const int tpr = BLOCK ? (int)blockDim.x : 32;
-  const int t = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & 31);
-  const int group = BLOCK ? 0 : (int)(threadIdx.x >> 5);
-  const long long r0 = BLOCK ? blockIdx.x : (long long)blockIdx.x * kRowsPerCta + group;
-  const long long step = BLOCK ? gridDim.x : (long long)gridDim.x * kRowsPerCta;
+  const Group<TPR, SUB> gr(a.lpr);
+  const int t = gr.t, tpr = gr.tpr, d = (int)a.d, S = a.ring;
   const T *x = (const T*)a.x, *r = (const T*)a.r;
   const TP *gm = (const TP*)a.gamma, *bt = (const TP*)a.beta;
-  const int d = (int)a.d, S = a.ring;
-  const uint32_t bytes = (uint32_t)(d * sizeof(T));
-  const uint32_t stage = bytes * (r ? 2u : 1u);
-  unsigned char* mem = ring_mem + (size_t)group * S * stage;
-  uint64_t* bar = bars + group * kMaxRing;
-  if (t == 0) {
-    for (int i = 0; i < S; ++i) ring_init(&bar[i]);
-    ring_init_done();
+  const uint32_t region = region_bytes(d, sizeof(T), gr.rpw, ELEM), stage = region * (r ? 2u : 1u);
+  const uint32_t mem = tc::smem_u32(ring_mem) + (uint32_t)gr.index * S * stage;
+  uint64_t* bar = bars + gr.index * kMaxRing;
+  if (gr.lane == 0) {
+    for (int i = 0; i < S; ++i) tc::mbar_init(&bar[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::fence_async_smem();
   }
   pdl_begin();
-  auto fill = [&](long long row, int st) {
-    tc::mbar_expect_tx(&bar[st], stage);
-    const uint32_t dst = tc::smem_u32(mem) + st * stage;
-    bulk_load(dst, x + row * a.ldx, bytes, &bar[st]);
-    if (r) bulk_load(dst + bytes, r + row * a.ldr, bytes, &bar[st]);
+  auto rows_of = [&](long long rb) { return SUB ? (int)min((long long)gr.rpw, a.rows - rb * gr.rpw) : 1; };
+  auto fill = [&](long long rb, int st) {
+    const int n = rows_of(rb);
+    tc::mbar_expect_tx(&bar[st], fill_bytes<T, ELEM>(x, a.ldx, d, rb, gr.rpw, n) +
+                                     (r ? fill_bytes<T, ELEM>(r, a.ldr, d, rb, gr.rpw, n) : 0u));
+    fill_region<T, SUB, ELEM>(mem + st * stage, x, a.ldx, d, rb, gr.rpw, n, &bar[st]);
+    if (r) fill_region<T, SUB, ELEM>(mem + st * stage + region, r, a.ldr, d, rb, gr.rpw, n, &bar[st]);
   };
-  if (t == 0)
+  const long long blocks = SUB ? (a.rows + gr.rpw - 1) / gr.rpw : a.rows;
+  if (gr.lane == 0)
     for (int i = 0; i < S; ++i)
-      if (r0 + i * step < a.rows) fill(r0 + i * step, i);
-  if (BLOCK) __syncthreads();
-  else __syncwarp();
+      if (gr.first + i * gr.step < blocks) fill(gr.first + i * gr.step, i);
+  gr.sync();
+  // this thread's edge elements of row ``row``
+  T ex = T(0.f), er = T(0.f);
+  auto edges = [&](long long row) {
+    if (!ELEM || gr.lane >= kEdgeThreads || row >= a.rows) return;
+    const int i = edge_index(edges_of(x + row * a.ldx, d), d, gr.lane);
+    if (i >= 0) ex = x[row * a.ldx + i];
+    if (r) {
+      const int j = edge_index(edges_of(r + row * a.ldr, d), d, gr.lane);
+      if (j >= 0) er = r[row * a.ldr + j];
+    }
+  };
+  auto put_edge = [&](uint32_t where, const T* row, T v) {
+    const Edges e = edges_of(row, d);
+    const int i = edge_index(e, d, gr.lane);
+    if (i >= 0) *reinterpret_cast<T*>(ring_mem + (where - tc::smem_u32(ring_mem)) + e.off + i * sizeof(T)) = v;
+  };
+  edges(gr.first);
+  const int left = ELEM ? d - t : (d - t * VEC + VEC - 1) / VEC;  // elements (vectors: elements / VEC) from this thread's on
   bool in[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) in[i] = (i * tpr + t) * VEC < d;
-  Param<T, TP> pg[NV], pb[NV];
+  for (int i = 0; i < NV; ++i) in[i] = ELEM ? i * VEC * TPR < left : (i * tpr + t) * VEC < d;
+  ParamPart<T, TP, ELEM, TPR> pg[NV], pb[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (in[i]) {
-      if (gm) pg[i].load(gm + (i * tpr + t) * VEC);
-      if (bt) pb[i].load(bt + (i * tpr + t) * VEC);
+      if (gm) pg[i].load(gm + t * (ELEM ? 1 : VEC), i, tpr, left);
+      if (bt) pb[i].load(bt + t * (ELEM ? 1 : VEC), i, tpr, left);
     }
   const float inv_d = 1.0f / (float)d;
-  int turn = 0, st = 0, before = S - 1;  // this row's stage and the previous row's
+  int turn = 0, st = 0, before = S - 1;  // this block's stage and the one before's
   uint32_t ph = 0;
-  for (long long row = r0; row < a.rows; row += step) {
+  for (long long rb = gr.first; rb < blocks; rb += gr.step) {
+    const long long row = rb * gr.rpw + gr.sub;
+    const bool on = !SUB || row < a.rows;
+    uint32_t m = mem + st * stage;
+    uint32_t mr = m + region;
+    if (ELEM) {
+      if (gr.lane < kEdgeThreads) {
+        put_edge(m, x + row * a.ldx, ex);
+        if (r) put_edge(mr, r + row * a.ldr, er);
+      }
+      edges(row + gr.step);
+      m += (uint32_t)((uintptr_t)(x + row * a.ldx) & 15) + t * sizeof(T);
+      if (r) mr += (uint32_t)((uintptr_t)(r + row * a.ldr) & 15) + t * sizeof(T);
+    } else {
+      m += gr.sub * (uint32_t)(d * sizeof(T)) + t * 16;
+      mr += gr.sub * (uint32_t)(d * sizeof(T)) + t * 16;
+    }
     ring_wait(&bar[st], ph);
-    const unsigned char* m = mem + (size_t)st * stage + t * 16;
+    if (ELEM) gr.sync();
     f32x2 v[NV][P];
     f32x2 sum = 0;  // two zeros
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < P; ++j) v[i][j] = 0;
-      if (in[i]) {
-        widen(*reinterpret_cast<const uint4*>(m + i * tpr * 16), v[i], T());
+      if (in[i] && on) {
+        row_get<T, ELEM, TPR>(m, i, tpr, left, v[i]);
         if (r) {
           f32x2 w[P];
-          widen(*reinterpret_cast<const uint4*>(m + bytes + i * tpr * 16), w, T());
+          row_get<T, ELEM, TPR>(mr, i, tpr, left, w);
 #pragma unroll
           for (int j = 0; j < P; ++j) v[i][j] = add2(v[i][j], w[j]);
         }
@@ -266,17 +466,11 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_fwd_ring(const FwdAr
         for (int j = 0; j < P; ++j) sum = add2(sum, v[i][j]);
       }
     }
-    float mu;
-    if (BLOCK) {
-      mu = block_sum2(sum2(sum), 0.f, buf, turn).x * inv_d;
-      // past that barrier every thread is done with the previous row's stage
-      const long long next = row + (S - 1) * step;
-      if (t == 0 && row != r0 && next < a.rows) fill(next, before);
-    } else {
-      mu = warp_sum(sum2(sum)) * inv_d;
-      const long long next = row + S * step;
-      if (t == 0 && next < a.rows) fill(next, st);  // the row is in registers
-    }
+    const float mu = gr.sum(sum2(sum), buf, turn) * inv_d;
+    // A warp has its rows in registers; a CTA's threads are all done with the
+    // row before this one.
+    const long long next = rb + (BLOCK ? S - 1 : S) * gr.step;
+    if (gr.lane == 0 && next < blocks && (!BLOCK || rb != gr.first)) fill(next, BLOCK ? before : st);
     before = st;
     if (++st == S) { st = 0; ph ^= 1u; }
     const f32x2 nmu = pair(-mu, -mu);
@@ -286,25 +480,31 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_fwd_ring(const FwdAr
       if (in[i]) {
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const f32x2 e = add2(v[i][j], nmu);
+          f32x2 e = add2(v[i][j], nmu);
+          if (ELEM) {  // elements past the row are zeros, not members of the sum
+            float e0, e1;
+            unpair(e, e0, e1);
+            e = pair((i * VEC + 2 * j) * TPR < left ? e0 : 0.f, (i * VEC + 2 * j + 1) * TPR < left ? e1 : 0.f);
+          }
           sq = fma2(e, e, sq);
         }
       }
-    const float var = (BLOCK ? block_sum2(sum2(sq), 0.f, buf, turn).x : warp_sum(sum2(sq))) * inv_d;
+    const float var = gr.sum(sum2(sq), buf, turn) * inv_d;
     const float rs = 1.0f / sqrtf(var + a.eps);
+    if (!on) continue;
     if (t == 0) {
       if (a.mean) a.mean[row] = mu;
       if (a.rstd) a.rstd[row] = rs;
     }
     const f32x2 rs2 = pair(rs, rs);
-    T* yo = (T*)a.y + row * a.ldy + t * VEC;
-    T* so = (T*)a.s + row * a.lds + t * VEC;
+    T* yo = (T*)a.y + row * a.ldy + t * (ELEM ? 1 : VEC);
+    T* so = (T*)a.s + row * a.lds + t * (ELEM ? 1 : VEC);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       // the stored sum is rounded to the matrix type; the norm itself uses
       // the unrounded one
-      if (a.s) *reinterpret_cast<uint4*>(so + i * tpr * VEC) = narrow(v[i], T());
+      if (a.s) row_put<T, ELEM, TPR>(so, i, tpr, left, v[i]);
       f32x2 e[P], w[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) e[j] = mul2(add2(v[i][j], nmu), rs2);
@@ -318,69 +518,8 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_fwd_ring(const FwdAr
 #pragma unroll
         for (int j = 0; j < P; ++j) e[j] = add2(e[j], w[j]);
       }
-      *reinterpret_cast<uint4*>(yo + i * tpr * VEC) = narrow(e, T());
+      row_put<T, ELEM, TPR>(yo, i, tpr, left, e);
     }
-  }
-}
-
-// The element-by-element kernel, for rows that start anywhere: TPR threads a
-// row (a warp, kRowsPerCta rows a CTA, or the CTA), NV elements a thread.
-template <typename T, typename TP, int NV, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kRowsPerCta : TPR) k_ln_fwd(const FwdArgs a) {
-  constexpr bool BLOCK = TPR > 32;
-  __shared__ float2 buf[2][32];
-  pdl_begin();
-  const int t = (int)threadIdx.x % TPR;
-  const long long r0 = BLOCK ? blockIdx.x : (long long)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
-  const long long step = BLOCK ? gridDim.x : (long long)gridDim.x * kRowsPerCta;
-  const TP *gm = (const TP*)a.gamma, *bt = (const TP*)a.beta;
-  const int left = (int)a.d - t;  // element i of this thread is i * TPR < left
-  const float inv_d = 1.0f / (float)(int)a.d;
-  float g[NV], b[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    g[i] = gm && i * TPR < left ? as_f32(gm[i * TPR + t]) : 1.f;
-    b[i] = bt && i * TPR < left ? as_f32(bt[i * TPR + t]) : 0.f;
-  }
-  int turn = 0;
-  for (long long row = r0; row < a.rows; row += step) {
-    const T* x = (const T*)a.x + row * a.ldx + t;
-    float v[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = i * TPR < left ? as_f32(x[i * TPR]) : 0.f;
-    if (a.r) {
-      const T* r = (const T*)a.r + row * a.ldr + t;
-      T w[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * TPR < left) w[i] = r[i * TPR];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * TPR < left) v[i] += as_f32(w[i]);
-    }
-    float sum = 0.f, sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sum += v[i];
-    const float mu = (BLOCK ? block_sum2(sum, 0.f, buf, turn).x : warp_sum(sum)) * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * TPR < left) sq = fmaf(v[i] - mu, v[i] - mu, sq);
-    const float var = (BLOCK ? block_sum2(sq, 0.f, buf, turn).x : warp_sum(sq)) * inv_d;
-    const float rs = 1.0f / sqrtf(var + a.eps);
-    if (t == 0) {
-      if (a.mean) a.mean[row] = mu;
-      if (a.rstd) a.rstd[row] = rs;
-    }
-    if (a.s) {
-      T* so = (T*)a.s + row * a.lds + t;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * TPR < left) so[i * TPR] = from_f32<T>(v[i]);
-    }
-    T* yo = (T*)a.y + row * a.ldy + t;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * TPR < left) yo[i * TPR] = from_f32<T>((v[i] - mu) * rs * g[i] + b[i]);
   }
 }
 
@@ -426,11 +565,12 @@ struct BwdArgs {
   void* dx;
   float* part;  // [grid][2][d] column sums of each CTA, or null
   long long rows, d, ldx, lddy, lddr, lddx;
-  int ring;  // stages of the pipelined kernels
+  int ring;  // stages
+  int lpr;   // lanes a row (warps)
+  uint32_t ring_bytes;
 };
 
-// dx = rstd (g - mean(g) - xh mean(g xh)) as g rstd + A + B x with
-// A = rstd (mean xh-term, below) and B = -rstd^2 mean(g xh): the row's two
+// dx = rstd (g - mean(g) - xh mean(g xh)) as g rstd + A + B x: the row's two
 // numbers are folded once instead of recomputing xh for every element.
 struct RowFold {
   float A, B;
@@ -442,48 +582,85 @@ __device__ __forceinline__ RowFold fold_row(float mu, float rs, float mg, float 
   return f;
 }
 
-template <typename T, typename TP, int NV, bool BLOCK, int MAXT>
-__global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_bwd_ring(const BwdArgs a) {
+template <typename T, typename TP, int NV, int TPR, bool SUB, bool ELEM, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
   constexpr int VEC = Vec<T>::n, P = Vec<T>::pairs;
+  constexpr bool BLOCK = TPR != 32;
   extern __shared__ __align__(128) unsigned char ring_mem[];
   __shared__ float2 buf[2][32];
   __shared__ __align__(8) uint64_t bars[(BLOCK ? 1 : kRowsPerCta) * kMaxRing];
-  const int tpr = BLOCK ? (int)blockDim.x : 32;
-  const int t = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & 31);
-  const int group = BLOCK ? 0 : (int)(threadIdx.x >> 5);
-  const long long r0 = BLOCK ? blockIdx.x : (long long)blockIdx.x * kRowsPerCta + group;
-  const long long step = BLOCK ? gridDim.x : (long long)gridDim.x * kRowsPerCta;
+  const Group<TPR, SUB> gr(a.lpr);
+  const int t = gr.t, tpr = gr.tpr, d = (int)a.d, S = a.ring;
   const T *x = (const T*)a.x, *dy = (const T*)a.dy, *dr = (const T*)a.dr;
   const TP* gm = (const TP*)a.gamma;
-  const int d = (int)a.d, S = a.ring;
-  const uint32_t bytes = (uint32_t)(d * sizeof(T));
-  const uint32_t stage = bytes * (dr ? 3u : 2u);
-  unsigned char* mem = ring_mem + (size_t)group * S * stage;
-  uint64_t* bar = bars + group * kMaxRing;
-  if (t == 0) {
-    for (int i = 0; i < S; ++i) ring_init(&bar[i]);
-    ring_init_done();
+  const uint32_t region = region_bytes(d, sizeof(T), gr.rpw, ELEM), stage = region * (dr ? 3u : 2u);
+  const uint32_t mem = tc::smem_u32(ring_mem) + (uint32_t)gr.index * S * stage;
+  uint64_t* bar = bars + gr.index * kMaxRing;
+  if (gr.lane == 0) {
+    for (int i = 0; i < S; ++i) tc::mbar_init(&bar[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::fence_async_smem();
   }
   pdl_begin();
-  auto fill = [&](long long row, int st) {
-    tc::mbar_expect_tx(&bar[st], stage);
-    const uint32_t dst = tc::smem_u32(mem) + st * stage;
-    bulk_load(dst, x + row * a.ldx, bytes, &bar[st]);
-    bulk_load(dst + bytes, dy + row * a.lddy, bytes, &bar[st]);
-    if (dr) bulk_load(dst + 2 * bytes, dr + row * a.lddr, bytes, &bar[st]);
+  auto rows_of = [&](long long rb) { return SUB ? (int)min((long long)gr.rpw, a.rows - rb * gr.rpw) : 1; };
+  auto fill = [&](long long rb, int st) {
+    const int n = rows_of(rb);
+    tc::mbar_expect_tx(&bar[st], fill_bytes<T, ELEM>(x, a.ldx, d, rb, gr.rpw, n) +
+                                     fill_bytes<T, ELEM>(dy, a.lddy, d, rb, gr.rpw, n) +
+                                     (dr ? fill_bytes<T, ELEM>(dr, a.lddr, d, rb, gr.rpw, n) : 0u));
+    fill_region<T, SUB, ELEM>(mem + st * stage, x, a.ldx, d, rb, gr.rpw, n, &bar[st]);
+    fill_region<T, SUB, ELEM>(mem + st * stage + region, dy, a.lddy, d, rb, gr.rpw, n, &bar[st]);
+    if (dr) fill_region<T, SUB, ELEM>(mem + st * stage + 2 * region, dr, a.lddr, d, rb, gr.rpw, n, &bar[st]);
   };
-  if (t == 0)
+  const long long blocks = SUB ? (a.rows + gr.rpw - 1) / gr.rpw : a.rows;
+  if (gr.lane == 0)
     for (int i = 0; i < S; ++i)
-      if (r0 + i * step < a.rows) fill(r0 + i * step, i);
+      if (gr.first + i * gr.step < blocks) fill(gr.first + i * gr.step, i);
+  gr.sync();
+  T ex = T(0.f), ey = T(0.f), er = T(0.f);  // this thread's edge elements
+  auto edge = [&](const T* row) {
+    const int i = edge_index(edges_of(row, d), d, gr.lane);
+    return i >= 0 ? row[i] : T(0.f);
+  };
+  auto edges = [&](long long row) {
+    if (!ELEM || gr.lane >= kEdgeThreads || row >= a.rows) return;
+    ex = edge(x + row * a.ldx);
+    ey = edge(dy + row * a.lddy);
+    if (dr) er = edge(dr + row * a.lddr);
+  };
+  auto put_edge = [&](uint32_t where, const T* row, T v) {
+    const Edges e = edges_of(row, d);
+    const int i = edge_index(e, d, gr.lane);
+    if (i >= 0) *reinterpret_cast<T*>(ring_mem + (where - tc::smem_u32(ring_mem)) + e.off + i * sizeof(T)) = v;
+  };
+  edges(gr.first);
+  const int left = ELEM ? d - t : (d - t * VEC + VEC - 1) / VEC;
   bool in[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) in[i] = (i * tpr + t) * VEC < d;
-  // gamma waits in shared memory, behind the rings
-  TP* gs = reinterpret_cast<TP*>(ring_mem + (size_t)(BLOCK ? 1 : kRowsPerCta) * S * stage);
-  if (gm)
-    for (int c = threadIdx.x; c < d; c += blockDim.x) gs[c] = gm[c];
-  const uint32_t gsa = tc::smem_u32(gs) + t * VEC * (uint32_t)sizeof(TP);
-  __syncthreads();
+  for (int i = 0; i < NV; ++i) in[i] = ELEM ? i * VEC * TPR < left : (i * tpr + t) * VEC < d;
+  // gamma of this thread's columns: in registers (element form), else in
+  // shared memory behind the rings (registers would cost rows in flight)
+  ParamPart<T, TP, ELEM, TPR> pg[ELEM ? NV : 1];
+  const uint32_t gs = tc::smem_u32(ring_mem) + a.ring_bytes;
+  if (ELEM && gm) {
+#pragma unroll
+    for (int i = 0; i < (ELEM ? NV : 1); ++i) pg[i].load(gm + t, i, tpr, left);
+  }
+  if (!ELEM && gm) {
+    const uint4* from = reinterpret_cast<const uint4*>(gm);
+    uint4* to = reinterpret_cast<uint4*>(ring_mem + a.ring_bytes);
+    for (int c = threadIdx.x; c < d * (int)sizeof(TP) / 16; c += blockDim.x) to[c] = from[c];
+    __syncthreads();
+  }
+  auto gamma = [&](int i, f32x2 (&w)[P]) {
+    if constexpr (ELEM) {
+      pg[i].get(w);
+    } else {
+      Param<T, TP> g;
+      g.load_shared(gs + (i * tpr + t) * VEC * (uint32_t)sizeof(TP));
+      g.get(w);
+    }
+  };
   const float inv_d = 1.0f / (float)d;
   f32x2 dg[NV][P], db[NV][P];
 #pragma unroll
@@ -492,32 +669,49 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_bwd_ring(const BwdAr
     for (int j = 0; j < P; ++j) dg[i][j] = db[i][j] = 0;
   int turn = 0, st = 0, before = S - 1;
   uint32_t ph = 0;
-  float mu = 0.f, rs = 0.f;
-  if (r0 < a.rows) {
-    mu = a.mean[r0];
-    rs = a.rstd[r0];
-  }
-  for (long long row = r0; row < a.rows; row += step) {
-    float mu_next = 0.f, rs_next = 0.f;
-    if (row + step < a.rows) {
-      mu_next = a.mean[row + step];
-      rs_next = a.rstd[row + step];
+  auto stats = [&](long long rb, float& mu, float& rs) {
+    const long long row = rb * gr.rpw + gr.sub;
+    mu = rs = 0.f;
+    if (row < a.rows) {
+      mu = a.mean[row];
+      rs = a.rstd[row];
+    }
+  };
+  float mu, rs;
+  stats(gr.first, mu, rs);
+  for (long long rb = gr.first; rb < blocks; rb += gr.step) {
+    const long long row = rb * gr.rpw + gr.sub;
+    const bool on = !SUB || row < a.rows;
+    float mu_next, rs_next;
+    stats(rb + gr.step, mu_next, rs_next);
+    uint32_t m = mem + st * stage, my = m + region, mr = my + region;
+    if (ELEM) {
+      if (gr.lane < kEdgeThreads) {
+        put_edge(m, x + row * a.ldx, ex);
+        put_edge(my, dy + row * a.lddy, ey);
+        if (dr) put_edge(mr, dr + row * a.lddr, er);
+      }
+      edges(row + gr.step);
+      m += (uint32_t)((uintptr_t)(x + row * a.ldx) & 15) + t * sizeof(T);
+      my += (uint32_t)((uintptr_t)(dy + row * a.lddy) & 15) + t * sizeof(T);
+      if (dr) mr += (uint32_t)((uintptr_t)(dr + row * a.lddr) & 15) + t * sizeof(T);
+    } else {
+      const uint32_t o = gr.sub * (uint32_t)(d * sizeof(T)) + t * 16;
+      m += o;
+      my += o;
+      mr += o;
     }
     ring_wait(&bar[st], ph);
-    const uint32_t m = tc::smem_u32(mem) + st * stage + t * 16;
+    if (ELEM) gr.sync();
     f32x2 sg = 0, sgx = 0;
     const f32x2 nmu = pair(-mu, -mu), rs2 = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
+      if (!in[i] || !on) continue;
       f32x2 xv[P], yv[P], w[P];
-      widen(lds128(m + i * tpr * 16), xv, T());
-      widen(lds128(m + bytes + i * tpr * 16), yv, T());
-      if (gm) {
-        Param<T, TP> pg;
-        pg.load_shared(gsa + i * tpr * VEC * (uint32_t)sizeof(TP));
-        pg.get(w);
-      }
+      row_get<T, ELEM, TPR>(m, i, tpr, left, xv);
+      row_get<T, ELEM, TPR>(my, i, tpr, left, yv);  // zero past the row, and with it every product below
+      if (gm) gamma(i, w);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const f32x2 xh = mul2(add2(xv[j], nmu), rs2);
@@ -528,50 +722,40 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_bwd_ring(const BwdAr
         db[i][j] = add2(db[i][j], yv[j]);
       }
     }
-    float mg = sum2(sg), mgx = sum2(sgx);
+    const float2 s = gr.sum(sum2(sg), sum2(sgx), buf, turn);
+    // past a CTA's barrier every thread is done with the row before this one
     if (BLOCK) {
-      const float2 s = block_sum2(mg, mgx, buf, turn);
-      mg = s.x;
-      mgx = s.y;
-      // past that barrier every thread is done with the previous row's stage
-      const long long next = row + (S - 1) * step;
-      if (t == 0 && row != r0 && next < a.rows) fill(next, before);
-    } else {
-      mg = warp_sum(mg);
-      mgx = warp_sum(mgx);
+      const long long next = rb + (S - 1) * gr.step;
+      if (gr.lane == 0 && next < blocks && rb != gr.first) fill(next, before);
     }
-    if (a.dx) {
-      const RowFold f = fold_row(mu, rs, mg * inv_d, mgx * inv_d);
+    if (a.dx && on) {
+      const RowFold f = fold_row(mu, rs, s.x * inv_d, s.y * inv_d);
       const f32x2 A = pair(f.A, f.A), B = pair(f.B, f.B);
-      T* o = (T*)a.dx + row * a.lddx + t * VEC;
+      T* o = (T*)a.dx + row * a.lddx + t * (ELEM ? 1 : VEC);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
         f32x2 xv[P], yv[P], w[P];
-        widen(lds128(m + i * tpr * 16), xv, T());
-        widen(lds128(m + bytes + i * tpr * 16), yv, T());
-        if (gm) {
-          Param<T, TP> pg;
-          pg.load_shared(gsa + i * tpr * VEC * (uint32_t)sizeof(TP));
-          pg.get(w);
-        }
+        row_get<T, ELEM, TPR>(m, i, tpr, left, xv);
+        row_get<T, ELEM, TPR>(my, i, tpr, left, yv);
+        if (gm) gamma(i, w);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           const f32x2 g = gm ? mul2(yv[j], w[j]) : yv[j];
           xv[j] = fma2(g, rs2, fma2(xv[j], B, A));
         }
         if (dr) {
-          widen(lds128(m + 2 * bytes + i * tpr * 16), w, T());
+          row_get<T, ELEM, TPR>(mr, i, tpr, left, w);
 #pragma unroll
           for (int j = 0; j < P; ++j) xv[j] = add2(xv[j], w[j]);
         }
-        *reinterpret_cast<uint4*>(o + i * tpr * VEC) = narrow(xv, T());
+        row_put<T, ELEM, TPR>(o, i, tpr, left, xv);
       }
     }
     if (!BLOCK) {
       __syncwarp();
-      const long long next = row + S * step;
-      if (t == 0 && next < a.rows) fill(next, st);
+      const long long next = rb + S * gr.step;
+      if (gr.lane == 0 && next < blocks) fill(next, st);
     }
     before = st;
     if (++st == S) { st = 0; ph ^= 1u; }
@@ -580,116 +764,54 @@ __global__ void __launch_bounds__(MAXT, BLOCK ? 1 : 2) k_ln_bwd_ring(const BwdAr
   }
   if (!a.part) return;
   float* out = a.part + (long long)blockIdx.x * 2 * d;
-  if (BLOCK) {  // every thread has columns of its own
+  // A CTA's threads have columns of their own.  A warp's sums go where its
+  // ring was (two stages hold them), after those of its several rows have met,
+  // and the CTA adds its warps' in order.
+  float* mine = BLOCK ? out : reinterpret_cast<float*>(ring_mem + (size_t)gr.index * S * stage);
+  if (!BLOCK) {
+    __syncwarp();
+    for (int o = tpr; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          dg[i][j] = add2(dg[i][j], __shfl_xor_sync(0xffffffffu, dg[i][j], o));
+          db[i][j] = add2(db[i][j], __shfl_xor_sync(0xffffffffu, db[i][j], o));
+        }
+    }
+  }
+  if (gr.sub == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
-      const int c = (i * tpr + t) * VEC;
+      if (ELEM) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        *reinterpret_cast<f32x2*>(out + c + 2 * j) = dg[i][j];
-        *reinterpret_cast<f32x2*>(out + d + c + 2 * j) = db[i][j];
+        for (int j = 0; j < VEC; ++j) {
+          const int k = (i * VEC + j) * TPR;
+          float g0, g1, b0, b1;
+          unpair(dg[i][j / 2], g0, g1);
+          unpair(db[i][j / 2], b0, b1);
+          if (k < left) {
+            mine[t + k] = j & 1 ? g1 : g0;
+            mine[d + t + k] = j & 1 ? b1 : b0;
+          }
+        }
+      } else {
+        const int c = (i * tpr + t) * VEC;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          *reinterpret_cast<f32x2*>(mine + c + 2 * j) = dg[i][j];
+          *reinterpret_cast<f32x2*>(mine + d + c + 2 * j) = db[i][j];
+        }
       }
     }
-    return;
   }
-  // a warp's sums go where its ring was (a ring of two rows holds them), then
-  // the CTA adds its warps' in order
-  float* mine = reinterpret_cast<float*>(mem);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!in[i]) continue;
-    const int c = (i * 32 + t) * VEC;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      *reinterpret_cast<f32x2*>(mine + c + 2 * j) = dg[i][j];
-      *reinterpret_cast<f32x2*>(mine + d + c + 2 * j) = db[i][j];
-    }
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRowsPerCta; ++w) v += reinterpret_cast<const float*>(ring_mem + (size_t)w * S * stage)[c];
-    out[c] = v;
-  }
-}
-
-template <typename T, typename TP, int NV, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kRowsPerCta : TPR) k_ln_bwd(const BwdArgs a) {
-  constexpr bool BLOCK = TPR > 32;
-  __shared__ float2 buf[2][32];
-  extern __shared__ float cols[];  // a warp a row: [warps][2][d] column sums
-  pdl_begin();
-  const int t = (int)threadIdx.x % TPR;
-  const long long r0 = BLOCK ? blockIdx.x : (long long)blockIdx.x * kRowsPerCta + (threadIdx.x >> 5);
-  const long long step = BLOCK ? gridDim.x : (long long)gridDim.x * kRowsPerCta;
-  const TP* gm = (const TP*)a.gamma;
-  const int d = (int)a.d, left = d - t;  // element i of this thread is i * TPR < left
-  const float inv_d = 1.0f / (float)d;
-  float gam[NV], dg[NV], db[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    gam[i] = gm && i * TPR < left ? as_f32(gm[i * TPR + t]) : 1.f;
-    dg[i] = db[i] = 0.f;
-  }
-  int turn = 0;
-  for (long long row = r0; row < a.rows; row += step) {
-    const T *x = (const T*)a.x + row * a.ldx + t, *dy = (const T*)a.dy + row * a.lddy + t;
-    const float mu = a.mean[row], rs = a.rstd[row];
-    T px[NV], py[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * TPR < left) {
-        px[i] = x[i * TPR];
-        py[i] = dy[i * TPR];
-      }
-    float mg = 0.f, mgx = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * TPR < left) {
-        const float xh = (as_f32(px[i]) - mu) * rs, y = as_f32(py[i]), g = y * gam[i];
-        mg += g;
-        mgx = fmaf(g, xh, mgx);
-        dg[i] = fmaf(y, xh, dg[i]);
-        db[i] += y;
-      }
-    if (!a.dx) continue;
-    if (BLOCK) {
-      const float2 s = block_sum2(mg, mgx, buf, turn);
-      mg = s.x;
-      mgx = s.y;
-    } else {
-      mg = warp_sum(mg);
-      mgx = warp_sum(mgx);
-    }
-    const RowFold f = fold_row(mu, rs, mg * inv_d, mgx * inv_d);
-    T* o = (T*)a.dx + row * a.lddx + t;
-    const T* dr = a.dr ? (const T*)a.dr + row * a.lddr + t : nullptr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * TPR < left) {
-        float e = fmaf(as_f32(py[i]) * gam[i], rs, fmaf(as_f32(px[i]), f.B, f.A));
-        if (dr) e += as_f32(dr[i * TPR]);
-        o[i * TPR] = from_f32<T>(e);
-      }
-  }
-  if (!a.part) return;
-  float* out = a.part + (long long)blockIdx.x * 2 * d;
-  float* mine = BLOCK ? out : cols + (size_t)(threadIdx.x >> 5) * 2 * d;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (i * TPR < left) {
-      mine[i * TPR + t] = dg[i];
-      mine[d + i * TPR + t] = db[i];
-    }
   if (BLOCK) return;
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowsPerCta; ++w) v += cols[(size_t)w * 2 * d + c];
+    for (int w = 0; w < kRowsPerCta; ++w) v += reinterpret_cast<const float*>(ring_mem + (size_t)w * S * stage)[c];
     out[c] = v;
   }
 }
@@ -759,7 +881,7 @@ __global__ void __launch_bounds__(1024) k_ln_bwd_cols(const BwdArgs a, void* dga
 
 // dgamma and dbeta from the CTAs' column sums: 32 columns a CTA, the n sums of
 // a column dealt to its warps and added in a fixed order.
-constexpr int kReduceWarps = 16;
+constexpr int kReduceWarps = 32;
 __global__ void __launch_bounds__(32 * kReduceWarps) k_ln_bwd_reduce(const float* part, int n, long long d,
                                                                      void* dgamma, void* dbeta, int pf32,
                                                                      int accumulate) {
@@ -791,39 +913,73 @@ __global__ void __launch_bounds__(32 * kReduceWarps) k_ln_bwd_reduce(const float
 
 // ------------------------------------------------------------------ planning
 struct Plan {
-  bool vec;     // 16-byte vectors (the pipelined kernels), else element by element
-  int nv;       // vectors (elements) a thread
-  bool block;   // the CTA a row (else a warp a row)
+  bool elem;    // element by element (rows that start anywhere), else 16-byte vectors
+  int nv;       // vectors a thread
+  bool block;   // the CTA a row (else a warp, or lpr lanes of one)
   int threads;  // CTA size
-  bool wide;    // the row does not fit: the three-pass kernels
+  int lpr;
+  bool wide;    // the row does not fit: the kernels that walk it several times
+  int stages, per_sm;  // the ring, and CTAs a SM
+  size_t bytes;        // the rings' shared memory
+  size_t gamma;        // and gamma's behind it (backward)
 };
 
-// Vectors need 16-byte aligned rows and parameters and whole vectors a row;
-// other shapes go element by element, still coalesced.  A warp takes a row of
-// up to 4 vectors (16 elements) a lane, a CTA one of 16 elements a thread.
-static Plan plan(long long d, int es, bool aligned) {
-  Plan p;
-  p.vec = aligned && (d * es) % 16 == 0;
-  const int vec = p.vec ? 16 / es : 1;
-  const long long n = (d + vec - 1) / vec;
-  const int most = p.vec ? 4 : 16, cta = 16 / vec;  // vectors a lane, vectors a thread of a CTA
-  p.wide = n > (p.vec ? 1024LL : 512LL) * cta;
-  p.block = p.wide || n > 32LL * most;
+// A warp takes a row of up to 4 vectors a lane (several rows of up to half a
+// vector a lane), a CTA one of 16 elements a thread.  ``arrays``: input arrays
+// of a stage (3 for the backward, whose CTAs each leave a row of column sums
+// and are therefore kept to few a SM); pes: bytes of a gamma element.
+static Plan plan(long long d, int es, bool aligned, int arrays, int pes) {
+  Plan p = {};
+  const int vec = 16 / es;
+  p.elem = !(aligned && (d * es) % 16 == 0);
+  p.wide = d > (p.elem ? 512 * 16 : 1024 * 16);
+  p.block = !p.wide && d > (p.elem ? 32 * 16 : 32 * 4 * vec);
   p.nv = 1;
-  p.threads = p.wide ? 1024 : 32 * kRowsPerCta;
-  if (p.wide) return p;
-  if (!p.block) {
-    while (p.nv * 32 < n) p.nv = p.vec ? p.nv + 1 : p.nv * 2;
-  } else {
-    p.nv = cta;
-    p.threads = (int)(((n + cta - 1) / cta + 31) / 32 * 32);
-    if (!p.vec) {  // 64, 128, 256 or 512 threads: the offsets are then constants
+  p.lpr = 32;
+  p.threads = 32 * kRowsPerCta;
+  if (!p.wide && !p.block) {
+    while (p.nv * 32 * vec < d) ++p.nv;
+    if (p.elem && p.nv == 3) p.nv = 4;
+    if (!p.elem)
+      while (p.nv == 1 && p.lpr > 4 && p.lpr / 2 * vec >= d) p.lpr /= 2;
+  } else if (p.block) {
+    p.nv = 16 / vec;
+    p.threads = (int)((d + 16 * 32 - 1) / (16 * 32)) * 32;
+    if (p.elem) {  // 64, 128, 256 or 512 threads: the offsets are then constants
       int th = 64;
       while (th < p.threads) th *= 2;
       p.threads = th;
     }
   }
+  if (!p.wide) {
+    const size_t stage = (size_t)region_bytes(d, es, 32 / p.lpr, p.elem) * arrays * (p.block ? 1 : kRowsPerCta);
+    constexpr size_t kSm = 226 * 1024;  // of 227 KB; the static arrays take the rest
+    p.gamma = arrays == 3 && !p.elem ? (size_t)d * pes : 0;
+    const bool bwd = arrays == 3;
+    const int most = p.threads <= 128 ? (bwd ? 4 : 8) : (bwd ? 2 : 4);
+    int want = p.block ? (bwd ? 640 : 1024) / p.threads : 2;
+    want = want < 1 ? 1 : want > most ? most : want;
+    for (p.per_sm = want; p.per_sm > 1; --p.per_sm)
+      if (2 * stage + p.gamma <= kSm / p.per_sm - 1024) break;
+    const size_t room = kSm / p.per_sm - (p.per_sm > 1 ? 1024 : 0);  // 1 KB of every CTA's is the system's
+    p.stages = room > p.gamma ? (int)((room - p.gamma) / stage) : 0;
+    if (p.stages > kMaxRing) p.stages = kMaxRing;
+    p.bytes = p.stages * stage;
+    // the warps' column sums go where their rings were
+    if (p.stages < 2 || (!p.block && arrays == 3 && 2 * d * 4 > (long long)(p.bytes / kRowsPerCta))) p.wide = true;
+  }
+  if (p.wide) {
+    p.block = true;
+    p.threads = 1024;
+    p.per_sm = 2;
+  }
   return p;
+}
+
+static int grid_of(const Plan& p, long long rows) {
+  const long long per = p.block ? 1 : (long long)kRowsPerCta * (32 / p.lpr);
+  const long long most = (long long)device_sms() * p.per_sm, n = (rows + per - 1) / per;
+  return (int)(n < most ? n : most);
 }
 
 static bool rows_aligned(const aal_mat& m) {
@@ -851,86 +1007,40 @@ static aal_status launch_pdl(void (*k)(A...), dim3 grid, int threads, size_t sme
   return cuda_status(e);
 }
 
-// Calls f with the kernel's compile-time shape.  V: elements of a vector.
-template <int V, typename F>
+// Calls f with the kernel's compile-time shape: vectors a thread, threads a
+// row, several rows a warp, the element form, the largest CTA and CTAs a SM.
+// The forward's wide rows run two CTAs of 512 threads a SM (64 registers); the
+// backward's column sums need more registers than that leaves.
+template <typename T, bool BWD, typename F>
 static aal_status with_shape(const Plan& p, F f) {
-  constexpr int W = 32 * kRowsPerCta;
-  if (!p.vec) {
+  constexpr int W = 32 * kRowsPerCta, N = 16 / Vec<T>::n;
+  if (p.elem) {
     if (p.block) {
       switch (p.threads) {
-        case 64: return f.template scalar<16, 64>();
-        case 128: return f.template scalar<16, 128>();
-        case 256: return f.template scalar<16, 256>();
-        default: return f.template scalar<16, 512>();
+        case 64: return f.template run<N, 64, false, true, 64, 8>();
+        case 128: return f.template run<N, 128, false, true, 128, 4>();
+        case 256: return f.template run<N, 256, false, true, 256, 2>();
+        default: return f.template run<N, 512, false, true, 512, BWD ? 1 : 2>();
       }
     }
     switch (p.nv) {
-      case 1: return f.template scalar<1, 32>();
-      case 2: return f.template scalar<2, 32>();
-      case 4: return f.template scalar<4, 32>();
-      case 8: return f.template scalar<8, 32>();
-      default: return f.template scalar<16, 32>();
+      case 1: return f.template run<1, 32, false, true, W, 2>();
+      case 2: return f.template run<2, 32, false, true, W, 2>();
+      default: return f.template run<N, 32, false, true, W, 2>();
     }
   }
-  if (p.block) return p.threads <= 512 ? f.template ring<16 / V, true, 512>() : f.template ring<16 / V, true, 1024>();
+  if (p.block) {
+    if (BWD && p.threads <= 320) return f.template run<N, 0, false, false, 320, 2>();
+    return p.threads <= 512 ? f.template run<N, 0, false, false, 512, BWD ? 1 : 2>()
+                            : f.template run<N, 0, false, false, 1024, 1>();
+  }
   switch (p.nv) {
-    case 1: return f.template ring<1, false, W>();
-    case 2: return f.template ring<2, false, W>();
-    case 3: return f.template ring<3, false, W>();
-    default: return f.template ring<4, false, W>();
+    case 1:
+      return p.lpr < 32 ? f.template run<1, 32, true, false, W, 2>() : f.template run<1, 32, false, false, W, 2>();
+    case 2: return f.template run<2, 32, false, false, W, 2>();
+    case 3: return f.template run<3, 32, false, false, W, 2>();
+    default: return f.template run<4, 32, false, false, W, 2>();
   }
-}
-
-// Stages of a group's ring and CTAs of a SM: two CTAs a SM where a CTA's
-// rings of two stages fit half of its shared memory, and as many stages as
-// then fit, up to kMaxRing.
-struct Ring {
-  int stages;
-  int per_sm;
-  size_t bytes;
-};
-static Ring ring_plan(const Plan& p, long long d, int es, int arrays) {
-  const size_t extra = arrays == 3 ? (size_t)d * 4 : 0;  // gamma of the backward
-  Ring r = {0, 0, 0};
-  const size_t stage = (size_t)d * es * arrays * (p.block ? 1 : kRowsPerCta);
-  constexpr size_t kSm = 220 * 1024;
-  // registers: about 100 a thread of a row's CTA, at most 128 of a warp's row
-  int want = p.block ? 640 / p.threads : 2;
-  want = want < 1 ? 1 : want > 4 ? 4 : want;
-  for (r.per_sm = want; r.per_sm > 1; --r.per_sm)
-    if (2 * stage + extra <= kSm / r.per_sm) break;
-  r.stages = (int)((kSm / r.per_sm - extra) / stage);
-  if (r.stages > kMaxRing) r.stages = kMaxRing;
-  r.bytes = r.stages * stage + extra;
-  return r;
-}
-
-static int grid_of(const Plan& p, long long rows, int per_sm) {
-  const long long per = p.block ? 1 : kRowsPerCta;
-  const long long most = (long long)device_sms() * per_sm, n = (rows + per - 1) / per;
-  return (int)(n < most ? n : most);
-}
-// CTAs a SM of the kernels without a ring: what their registers allow for the
-// forward, few for the backward, whose CTAs each leave a row of column sums.
-static int plain_per_sm(const Plan& p, bool bwd) {
-  const int fit = 1024 / p.threads;
-  const int most = bwd ? 4 : 8;
-  return p.wide ? 2 : fit < 1 ? 1 : fit < most ? fit : most;
-}
-// A row whose ring does not hold two stages takes the three-pass kernels.
-static Plan ring_or_wide(Plan p, long long d, int es, int arrays) {
-  if (p.vec && !p.wide && ring_plan(p, d, es, arrays).stages < 2) {
-    p.wide = p.block = true;
-    p.threads = 1024;
-  }
-  return p;
-}
-static Plan fwd_plan(long long d, int es, bool aligned) { return ring_or_wide(plan(d, es, aligned), d, es, 2); }
-static Plan bwd_plan(long long d, int es, bool aligned) { return ring_or_wide(plan(d, es, aligned), d, es, 3); }
-// CTAs of the backward (its workspace holds two rows of sums for each).
-static int bwd_grid(const Plan& p, long long rows, long long d, int es) {
-  if (!p.vec) return grid_of(p, rows, plain_per_sm(p, true));
-  return grid_of(p, rows, ring_plan(p, d, es, 3).per_sm);
 }
 
 template <typename T, typename TP>
@@ -938,43 +1048,32 @@ struct FwdLaunch {
   FwdArgs a;
   const Plan& p;
   cudaStream_t s;
-  template <int NV, int TPR>
-  aal_status scalar() {
-    return launch_pdl(k_ln_fwd<T, TP, NV, TPR>, dim3((unsigned)grid_of(p, a.rows, plain_per_sm(p, false))), p.threads,
-                      0, s, a);
-  }
-  template <int NV, bool BLOCK, int MAXT>
-  aal_status ring() {
-    const Ring r = ring_plan(p, a.d, sizeof(T), a.r ? 2 : 1);
-    a.ring = r.stages;
-    return launch_pdl(k_ln_fwd_ring<T, TP, NV, BLOCK, MAXT>,
-                      dim3((unsigned)grid_of(p, a.rows, r.per_sm)), p.threads, r.bytes, s, a);
+  template <int NV, int TPR, bool SUB, bool ELEM, int MAXT, int MINB>
+  aal_status run() {
+    a.ring = p.stages;
+    a.lpr = p.lpr;
+    return launch_pdl(k_ln_fwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>, dim3((unsigned)grid_of(p, a.rows)), p.threads, p.bytes, s,
+                      a);
   }
 };
 template <typename T, typename TP>
 static aal_status run_fwd(const FwdArgs& a, const Plan& p, cudaStream_t s) {
-  if (p.wide)
-    return launch_pdl(k_ln_fwd_wide<T, TP>, dim3((unsigned)grid_of(p, a.rows, 2)), p.threads, 0, s, a);
-  return with_shape<16 / sizeof(T)>(p, FwdLaunch<T, TP>{a, p, s});
+  if (p.wide) return launch_pdl(k_ln_fwd_wide<T, TP>, dim3((unsigned)grid_of(p, a.rows)), p.threads, 0, s, a);
+  return with_shape<T, false>(p, FwdLaunch<T, TP>{a, p, s});
 }
 
 template <typename T, typename TP>
 struct BwdLaunch {
   BwdArgs a;
   const Plan& p;
-  int grid;
   cudaStream_t s;
-  template <int NV, int TPR>
-  aal_status scalar() {
-    return launch_pdl(k_ln_bwd<T, TP, NV, TPR>, dim3((unsigned)grid), p.threads,
-                      TPR == 32 ? (size_t)a.d * 2 * kRowsPerCta * sizeof(float) : 0, s, a);
-  }
-  template <int NV, bool BLOCK, int MAXT>
-  aal_status ring() {
-    // the stages fit three arrays; with two the ring is no longer, only lighter
-    const Ring r = ring_plan(p, a.d, sizeof(T), 3);
-    a.ring = r.stages;
-    return launch_pdl(k_ln_bwd_ring<T, TP, NV, BLOCK, MAXT>, dim3((unsigned)grid), p.threads, r.bytes, s, a);
+  template <int NV, int TPR, bool SUB, bool ELEM, int MAXT, int MINB>
+  aal_status run() {
+    a.ring = p.stages;
+    a.lpr = p.lpr;
+    a.ring_bytes = (uint32_t)p.bytes;
+    return launch_pdl(k_ln_bwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>, dim3((unsigned)grid_of(p, a.rows)), p.threads,
+                      p.bytes + p.gamma, s, a);
   }
 };
 
@@ -986,9 +1085,9 @@ static bool valid_vec(const aal_mat& m, long long d, int dtype) {
 }
 
 // Partial column sums of the backward: CTAs times two rows of d floats.
-static long long bwd_part_bytes(long long rows, long long d, int es, bool aligned) {
-  const Plan p = bwd_plan(d, es, aligned);
-  return p.wide ? 0 : (long long)bwd_grid(p, rows, d, es) * 2 * d * 4;
+static long long bwd_part_bytes(long long rows, long long d, int es, bool aligned, int pes) {
+  const Plan p = plan(d, es, aligned, 3, pes);
+  return p.wide ? 0 : (long long)grid_of(p, rows) * 2 * d * 4;
 }
 
 }  // namespace norm
@@ -1017,8 +1116,8 @@ aal_status aal_layer_norm_fwd(aal_mat X, aal_mat R, aal_mat gamma, aal_mat beta,
   const int pdt = gamma.ptr ? gamma.dtype : beta.ptr ? beta.dtype : dt;
   const bool al = norm::rows_aligned(X) && norm::rows_aligned(R) && norm::rows_aligned(S) && norm::rows_aligned(Y) &&
                   norm::rows_aligned(gamma) && norm::rows_aligned(beta);
-  const norm::Plan p = norm::fwd_plan(d, dt == AAL_F32 ? 4 : 2, al);
-  norm::FwdArgs a = {X.ptr, R.ptr, gamma.ptr, beta.ptr, S.ptr, Y.ptr, mean, rstd, M, d, X.ld, R.ld, S.ld, Y.ld, eps, 0};
+  const norm::Plan p = norm::plan(d, dt == AAL_F32 ? 4 : 2, al, R.ptr ? 2 : 1, 0);
+  norm::FwdArgs a = {X.ptr, R.ptr, gamma.ptr, beta.ptr, S.ptr, Y.ptr, mean, rstd, M, d, X.ld, R.ld, S.ld, Y.ld, eps, 0, 0};
   cudaStream_t s = (cudaStream_t)stream;
   const aal_status st = timed(AAL_KERNEL_NORM_FWD, s, [&] {
     if (dt == AAL_F32) return norm::run_fwd<float, float>(a, p, s);
@@ -1035,10 +1134,11 @@ int64_t aal_layer_norm_bwd_workspace_size(int64_t rows, int64_t cols) {
   // the largest of what the element types and alignments need
   long long n = 0;
   for (int es = 2; es <= 4; es += 2)
-    for (int al = 0; al < 2; ++al) {
-      const long long b = norm::bwd_part_bytes(rows, cols, es, al != 0);
-      n = b > n ? b : n;
-    }
+    for (int al = 0; al < 2; ++al)
+      for (int pes = es; pes <= 4; pes += 2) {
+        const long long b = norm::bwd_part_bytes(rows, cols, es, al != 0, pes);
+        n = b > n ? b : n;
+      }
   return n;
 }
 
@@ -1064,10 +1164,9 @@ aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const
   const int gdt = gamma.ptr ? gamma.dtype : dt;
   const bool al = norm::rows_aligned(X) && norm::rows_aligned(dY) && norm::rows_aligned(dR) &&
                   norm::rows_aligned(dX) && norm::rows_aligned(gamma);
-  const int es = dt == AAL_F32 ? 4 : 2;
-  const norm::Plan p = norm::bwd_plan(d, es, al);
-  norm::BwdArgs a = {X.ptr, gamma.ptr, dY.ptr, dR.ptr, mean, rstd, dX.ptr, nullptr, M, d, X.ld, dY.ld, dR.ld, dX.ld, 0};
-  const int grid = p.wide ? 0 : norm::bwd_grid(p, M, d, es);
+  const norm::Plan p = norm::plan(d, dt == AAL_F32 ? 4 : 2, al, 3, gdt == AAL_F32 ? 4 : 2);
+  norm::BwdArgs a = {X.ptr, gamma.ptr, dY.ptr, dR.ptr, mean, rstd, dX.ptr, nullptr, M, d, X.ld, dY.ld, dR.ld, dX.ld, 0, 0, 0};
+  const int grid = norm::grid_of(p, M);
   const unsigned gx = (unsigned)((d + 31) / 32);
   if ((d + 31) / 32 > 0x7fffffffLL) return AAL_ERR_UNSUPPORTED;
   uint64_t have = 0;
@@ -1084,16 +1183,16 @@ aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const
     a.part = parts ? ws : nullptr;
     if (e == AAL_OK && M > 0 && (dX.ptr || parts)) {
       if (p.wide) {  // (without column sums: parts is false)
-        const dim3 g((unsigned)norm::grid_of(p, M, 2));
+        const dim3 g((unsigned)grid);
         e = dt == AAL_F32     ? norm::launch_pdl(norm::k_ln_bwd_wide<float, float>, g, p.threads, 0, s, a)
             : gdt == AAL_F32 ? norm::launch_pdl(norm::k_ln_bwd_wide<__nv_bfloat16, float>, g, p.threads, 0, s, a)
                              : norm::launch_pdl(norm::k_ln_bwd_wide<__nv_bfloat16, __nv_bfloat16>, g, p.threads, 0, s, a);
       } else if (dt == AAL_F32) {
-        e = norm::with_shape<4>(p, norm::BwdLaunch<float, float>{a, p, grid, s});
+        e = norm::with_shape<float, true>(p, norm::BwdLaunch<float, float>{a, p, s});
       } else if (gdt == AAL_F32) {
-        e = norm::with_shape<8>(p, norm::BwdLaunch<__nv_bfloat16, float>{a, p, grid, s});
+        e = norm::with_shape<__nv_bfloat16, true>(p, norm::BwdLaunch<__nv_bfloat16, float>{a, p, s});
       } else {
-        e = norm::with_shape<8>(p, norm::BwdLaunch<__nv_bfloat16, __nv_bfloat16>{a, p, grid, s});
+        e = norm::with_shape<__nv_bfloat16, true>(p, norm::BwdLaunch<__nv_bfloat16, __nv_bfloat16>{a, p, s});
       }
     }
     if (e == AAL_OK && cols && (parts || M == 0))
