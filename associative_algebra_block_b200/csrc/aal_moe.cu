@@ -58,62 +58,94 @@ __device__ __forceinline__ unsigned long long order_key(double v) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-// One warp ranks the logits l[0..E) of an entry and writes its k choices.
-__device__ void rank_logits(const double* l, int E, int k, int renorm, int* ids, float* wts) {
+// Writes the entry's k choices: the experts of the k largest logits l[0..E),
+// ties to the lower index, NaN last, and their softmax weights.  Up to
+// kCountExperts an expert's place is the number of experts before it, counted
+// by 256 / E threads each; beyond that a warp picks the largest k times.
+constexpr int kCountExperts = 512;
+__device__ __forceinline__ void write_weights(const double* l, const double* top, int E, int k, int renorm, bool nan,
+                                              float* wts) {
   const int lane = threadIdx.x & 31;
-  // the lane's best of the experts lane, lane + 32, ... not yet taken
-  unsigned long long taken = 0;  // bit i: expert lane + 32 i (kMaxExperts fit)
-  unsigned long long best = 0;
-  int at = INT_MAX;
-  bool nan = false;
-  auto scan = [&] {
-    best = 0;
-    at = INT_MAX;
-    for (int e = lane, i = 0; e < E; e += 32, ++i) {
-      if ((taken >> i) & 1ull) continue;
-      const unsigned long long key = order_key(l[e]);
-      if (at == INT_MAX || key > best) { best = key; at = e; }
-    }
-  };
-  for (int e = lane; e < E; e += 32) nan |= isnan(l[e]);
-  nan = __any_sync(0xffffffffu, nan);
-  scan();
-  double mx = 0.0;
-  float sum = 0.f, mine = 0.f;  // lane j: the weight of choice j
-  for (int j = 0; j < k; ++j) {
-    // the largest key, then the lowest expert that has it
-    const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
-    const bool in_hi = (unsigned)(best >> 32) == hi;
-    const unsigned lo = __reduce_max_sync(0xffffffffu, in_hi ? (unsigned)best : 0u);
-    const int e = (int)__reduce_min_sync(0xffffffffu, in_hi && (unsigned)best == lo ? (unsigned)at : 0x7fffffffu);
-    const double v = l[e];
-    if (j == 0) mx = v;
-    const float p = nan ? NAN : expf((float)(v - mx));
-    sum += p;
-    if (lane == j) {
-      mine = p;
-      ids[j] = e;
-    }
-    if ((e & 31) == lane) {
-      taken |= 1ull << (e >> 5);
-      scan();
-    }
-  }
+  const double mx = top[0];
+  const float p = lane < k ? expf((float)(top[lane] - mx)) : 0.f;
+  float sum = p;
   if (!renorm) {  // the softmax over every logit
     sum = 0.f;
     for (int e = lane; e < E; e += 32) sum += expf((float)(l[e] - mx));
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  if (lane < k) wts[lane] = mine / sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < k) wts[lane] = nan ? NAN : p / sum;
+}
+__device__ void rank_logits(const double* l, unsigned long long* key, double* top, int E, int k, int renorm, int* ids,
+                            float* wts) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  bool nan = false;
+  for (int e = tid; e < E; e += kRouterThreads) {
+    nan |= isnan(l[e]);
+    key[e] = order_key(l[e]);
+  }
+  nan = __syncthreads_or(nan);
+  if (E <= kCountExperts) {
+    int per = 1;  // threads an expert, neighbours in a warp
+    while (per < 32 && E * per * 2 <= kRouterThreads) per *= 2;
+    for (int e0 = 0; e0 < E; e0 += kRouterThreads / per) {  // the whole CTA, for the shuffles
+      const int e = e0 + tid / per;
+      const unsigned long long mine = e < E ? key[e] : 0ull;
+      int before = 0;
+#pragma unroll 8
+      for (int j = tid % per; j < E; j += per) {
+        const unsigned long long other = key[j];
+        before += other > mine || (other == mine && j < e);
+      }
+      for (int o = per >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      if (e < E && tid % per == 0 && before < k) {
+        ids[before] = e;
+        top[before] = l[e];
+      }
+    }
+  } else if (tid < 32) {
+    // the lane's best of the experts lane, lane + 32, ... not yet taken
+    unsigned long long taken = 0;  // bit i: expert lane + 32 i (kMaxExperts fit)
+    unsigned long long best = 0;
+    int at = INT_MAX;
+    auto scan = [&] {
+      best = 0;
+      at = INT_MAX;
+      for (int e = lane, i = 0; e < E; e += 32, ++i) {
+        if ((taken >> i) & 1ull) continue;
+        if (at == INT_MAX || key[e] > best) { best = key[e]; at = e; }
+      }
+    };
+    scan();
+    for (int j = 0; j < k; ++j) {
+      // the largest key, then the lowest expert that has it
+      const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
+      const bool in_hi = (unsigned)(best >> 32) == hi;
+      const unsigned lo = __reduce_max_sync(0xffffffffu, in_hi ? (unsigned)best : 0u);
+      const int e = (int)__reduce_min_sync(0xffffffffu, in_hi && (unsigned)best == lo ? (unsigned)at : 0x7fffffffu);
+      if (lane == 0) {
+        ids[j] = e;
+        top[j] = l[e];
+      }
+      if ((e & 31) == lane) {
+        taken |= 1ull << (e >> 5);
+        scan();
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < 32) write_weights(l, top, E, k, renorm, nan, wts);
 }
 
 template <typename T, int VEC, int TB>
 __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThreads) k_moe_router(const RouterArgs a) {
-  constexpr int U = TB == 1 ? 8 : 4;  // weight loads in flight
+  constexpr int U = 16;  // weight loads in flight
   extern __shared__ double sm[];
+  __shared__ double top[kMaxTopK];
   double* part = sm;                                 // [TB][E] this CTA's sums
   double* red = part + (size_t)TB * a.E;             // [TB][VEC][threads]
-  double* xs = red + (size_t)TB * VEC * kRouterThreads;  // [TB][slice]
+  double* xs = red + (size_t)TB * VEC * kRouterThreads;  // [slice][TB]
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = threadIdx.x;
   pdl_release();
@@ -150,24 +182,24 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
       }
       if (c0 == 0 && r0 == lane_r) {
         // the entries' inputs, widened once, while the first weights are on their way
-        for (int i = tid; i < TB * nd; i += kRouterThreads) {
-          const int b = i / nd, r = i - b * nd;
-          xs[(size_t)b * ds + r] = b < nb ? widen(x[(long long)(b0 + b) * a.ldx + d0 + r]) : 0.0;
-        }
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+          for (int r = tid; r < nd; r += kRouterThreads)
+            xs[(size_t)r * TB + b] = b < nb ? widen(x[(long long)(b0 + b) * a.ldx + d0 + r]) : 0.0;
         __syncthreads();
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int r = r0 + i * rl;
         if (r >= nd) break;
-        double wv[VEC];
+        double xv[TB];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) wv[j] = widen(w[i][j]);
+        for (int b = 0; b < TB; ++b) xv[b] = xs[(size_t)r * TB + b];
 #pragma unroll
-        for (int b = 0; b < TB; ++b) {
-          const double xv = xs[(size_t)b * ds + r];
+        for (int j = 0; j < VEC; ++j) {
+          const double wv = widen(w[i][j]);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) acc[b][j] = fma(wv[j], xv, acc[b][j]);
+          for (int b = 0; b < TB; ++b) acc[b][j] = fma(wv, xv[b], acc[b][j]);
         }
       }
     }
@@ -180,6 +212,7 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
       const int bj = i / cvb, c = i - bj * cvb, e = (c0 + c) * VEC + bj % VEC;
       if (e < a.E) {
         double s = 0.0;
+#pragma unroll 8
         for (int l = 0; l < rl; ++l) s += red[(size_t)bj * kRouterThreads + l * cvb + c];
         part[(size_t)(bj / VEC) * a.E + e] = s;
       }
@@ -187,7 +220,8 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
     __syncthreads();
   }
   cl.sync();
-  double* logit = red;  // this CTA's entry
+  double* logit = red;        // this CTA's entry
+  unsigned long long* key = reinterpret_cast<unsigned long long*>(red + a.E);
   if (rank < nb) {
     for (int e = tid; e < a.E; e += kRouterThreads) {
       double s = 0.0;
@@ -196,20 +230,23 @@ __global__ void __cluster_dims__(kRouterCtas, 1, 1) __launch_bounds__(kRouterThr
       logit[e] = s;
     }
   }
-  cl.sync();  // the peers' sums have been read
-  if (rank >= nb || tid >= 32) return;
-  const int b = b0 + rank;
-  int* ids = a.ids + (long long)b * a.k;
-  float* wts = a.weights + (long long)b * a.k;
-  if (a.positions[b] < 0) {  // skipped: no expert, no output row
-    if (tid == 0) flag_device_error(kDevBounds);
-    if (tid < a.k) {
-      ids[tid] = -1;
-      wts[tid] = 0.f;
+  cl.barrier_arrive();  // the peers' sums have been read
+  if (rank < nb) {
+    const int b = b0 + rank;
+    int* ids = a.ids + (long long)b * a.k;
+    float* wts = a.weights + (long long)b * a.k;
+    if (a.positions[b] < 0) {  // skipped: no expert, no output row
+      if (tid == 0) flag_device_error(kDevBounds);
+      if (tid < a.k) {
+        ids[tid] = -1;
+        wts[tid] = 0.f;
+      }
+    } else {
+      __syncthreads();
+      rank_logits(logit, key, top, a.E, a.k, a.renorm, ids, wts);
     }
-    return;
   }
-  rank_logits(logit, a.E, a.k, a.renorm, ids, wts);
+  cl.barrier_wait();
 }
 
 // ------------------------------------------------- experts, tensor-core path
@@ -280,14 +317,15 @@ struct Tables {
   int* first;      // [E] place of the expert's first entry in ``slot``
   unsigned* tmask; // [E] row types of its entries
   unsigned* who;   // [E][words] its entries, one bit each
+  int* id;         // [B k] the router's choices
+  float* weight;   // [B k] and their weights
   int* slot;       // [B k] choices by expert, then by entry
-  int* entry;      // [B k] the choices' entries
-  float* weight;   // [B k] and weights
+  int* entry;      // [B k] and their entries
   int* type;       // [B]
   int words;
   __host__ __device__ static size_t bytes(int passes, int E, int B, int k) {
     const size_t words = (B + 31) / 32;
-    return (sizeof(Pass) * passes + sizeof(int) * ((2 + words) * E + 3 * (size_t)B * k + B) + 15) / 16 * 16;
+    return (sizeof(Pass) * passes + sizeof(int) * ((2 + words) * E + 4 * (size_t)B * k + B) + 15) / 16 * 16;
   }
   __device__ explicit Tables(unsigned char* p, const ExpertArgs& a) {
     words = (a.B + 31) / 32;
@@ -295,10 +333,11 @@ struct Tables {
     first = reinterpret_cast<int*>(pass + a.passes);
     tmask = reinterpret_cast<unsigned*>(first + a.E);
     who = tmask + a.E;
-    slot = reinterpret_cast<int*>(who + a.E * words);
+    id = reinterpret_cast<int*>(who + a.E * words);
+    weight = reinterpret_cast<float*>(id + a.B * a.k);
+    slot = reinterpret_cast<int*>(weight + a.B * a.k);
     entry = slot + a.B * a.k;
-    weight = reinterpret_cast<float*>(entry + a.B * a.k);
-    type = reinterpret_cast<int*>(weight + a.B * a.k);
+    type = entry + a.B * a.k;
   }
 };
 
@@ -310,15 +349,21 @@ struct Tables {
 __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& tb, int width) {
   __shared__ int s_passes;
   const int n = a.B * a.k, W = tb.words;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) tb.tmask[e] = 0u;
-  for (int i = threadIdx.x; i < a.E * W; i += blockDim.x) tb.who[i] = 0u;
+  for (int s = threadIdx.x; s < n; s += blockDim.x) {
+    const int e = __ldcg(a.ids + s);
+    const float w = __ldcg(a.weights + s);
+    tb.id[s] = e;
+    tb.weight[s] = w;
+  }
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const long long pos = a.positions[b];
+    const long long pos = __ldcg((const long long*)a.positions + b);
     tb.type[b] = pos < 0 ? 0 : (int)(pos % a.q);
   }
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) tb.tmask[e] = 0u;
+  for (int i = threadIdx.x; i < a.E * W; i += blockDim.x) tb.who[i] = 0u;
   __syncthreads();
   for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const int e = a.ids[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
+    const int e = tb.id[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
     if (e >= 0) {
       atomicOr(&tb.who[e * W + (b >> 5)], 1u << (b & 31));
       atomicOr(&tb.tmask[e], 1u << tb.type[b]);
@@ -355,13 +400,12 @@ __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& t
   }
   __syncthreads();
   for (int s = threadIdx.x; s < n; s += blockDim.x) {
-    const int e = a.ids[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
+    const int e = tb.id[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
     if (e < 0) continue;
     int at = tb.first[e] + __popc(tb.who[e * W + (b >> 5)] & ((1u << (b & 31)) - 1u));
     for (int w = 0; w < (b >> 5); ++w) at += __popc(tb.who[e * W + w]);
     tb.slot[at] = s;
     tb.entry[at] = b;
-    tb.weight[at] = a.weights[s];
   }
   __syncthreads();
   return s_passes;
@@ -444,10 +488,10 @@ struct Ring {
     get = p + t * 512 + ((g ^ (2 * t)) << 4);
     xpos = p + 2048 + lane * 8;
   }
-  // Issues the copies of the walk's step (a group of its own).
-  __device__ __forceinline__ void issue(const Walk<NT>& k) {
-    const uint32_t chunk = threadIdx.x & 7;
-    const uint32_t d = put + head, dx = xpos + head;
+  // Issues the copies of the walk's step: its weights, and its entries'
+  // inputs.
+  __device__ __forceinline__ void issue_weights(const Walk<NT>& k) {
+    const uint32_t chunk = threadIdx.x & 7, d = put + head;
     const __nv_bfloat16* w = k.at;
     const long long four = 4 * k.ldw;
 #pragma unroll
@@ -455,10 +499,13 @@ struct Ring {
       copy(d + i * 512 + ((chunk ^ (2 * i)) << 4), w, k.wsize);
       w += four;
     }
+  }
+  __device__ __forceinline__ void issue_inputs(const Walk<NT>& k) {
+    const uint32_t dx = xpos + head;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) copy8(dx + nt * 256, k.x[nt] + k.k, k.xsize[nt]);
-    head = head + kStep == S * kStep ? 0 : head + kStep;
   }
+  __device__ __forceinline__ void advance() { head = head + kStep == S * kStep ? 0 : head + kStep; }
   // The products of the oldest step.
   __device__ __forceinline__ void multiply(float (&acc)[4][NT][4]) {
     const uint32_t s = get + tail, sx = xpos + tail;
@@ -511,23 +558,40 @@ struct Sums {
 // The loop both expert kernels share: ``open(i, walk)`` describes piece i of
 // this CTA for the calling warp, ``steps(i)`` is that warp's number of steps of
 // it, and ``close(i)`` runs after its sums are in red[warp] (no barrier yet).
-// All warps of the CTA close every piece.
-template <int NT, int S, typename Open, typename Steps, typename Close>
+// All warps of the CTA close every piece.  ``ready`` is called once, before the
+// first input is read and after the first steps' weights are on their way.
+template <int NT, int S, typename Open, typename Steps, typename Close, typename Ready>
 __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, int law, int pieces, Open open,
-                                           Steps steps, Close close) {
+                                           Steps steps, Close close, Ready ready) {
   Ring<NT, S> ring(ring_mem);
   Walk<NT> walk;
   walk.left = 0;
   int ahead = 0;  // next piece to open
-  auto produce = [&] {
+  auto produce_weights = [&] {
     while (!walk.left && ahead < pieces) open(ahead++, walk);
     if (walk.left) {
-      ring.issue(walk);
+      ring.issue_weights(walk);
+      ring.advance();
+      walk.next(law);
+    }
+  };
+  for (int i = 0; i < S - 1; ++i) produce_weights();
+  ready();
+  // the same steps again, for their inputs
+  walk.left = 0;
+  ahead = 0;
+  ring.head = 0;
+  auto produce = [&](bool weights) {
+    while (!walk.left && ahead < pieces) open(ahead++, walk);
+    if (walk.left) {
+      if (weights) ring.issue_weights(walk);
+      ring.issue_inputs(walk);
+      ring.advance();
       walk.next(law);
     }
     copy_commit();  // empty once the work has run out, so that the waits still count
   };
-  for (int i = 0; i < S - 1; ++i) produce();
+  for (int i = 0; i < S - 1; ++i) produce(false);
   float* mine = red + (threadIdx.x >> 5) * Sums<NT>::kFloats;
   for (int i = 0; i < pieces; ++i) {
     float acc[4][NT][4] = {};
@@ -535,7 +599,7 @@ __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, 
       copy_wait<S - 2>();  // the oldest step's copies of this lane have landed,
       __syncwarp();        // and so have the others'; nor does any still read the slot before it
       ring.multiply(acc);
-      produce();           // into the slot read in the round before
+      produce(true);       // into the slot read in the round before
     }
     Sums<NT>::put(mine, acc);
     close(i);
@@ -632,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
     if (shared) cl.sync();
     else __syncthreads();
   };
-  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close);
+  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close, [] {});
 }
 
 // 64 columns of y a cluster.  Its CTAs take the passes in turn, add every
@@ -655,8 +719,10 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
   const int bi = a.F / a.q, bo = a.D / a.q, spg = bi >> 4;
   const int kg = tile / a.tiles, c0 = kg * bo + (tile - kg * a.tiles) * kTile;
   const int width = min(kTile, (kg + 1) * bo - c0);
-  pdl_wait();
-  pdl_release();
+  // The router's results are complete here although this kernel has not waited
+  // yet: it starts once every CTA of k_moe_up has released it, which each does
+  // after its own wait for the router.  So the tables and the first weights
+  // come in while k_moe_up still runs; only its h needs the wait.
   const int np = build_tables(a, tb, 8 * NT);
   const int whole = np / kDownCtas, left = np - whole * kDownCtas;
   const int z = left > 4 ? 1 : left > 2 ? 2 : left == 2 ? 4 : 8;  // CTAs that share a left-over pass
@@ -695,11 +761,14 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) s += red[w * kRed + o];
-      ys[tb.entry[p.first + m] * kTile + c] += tb.weight[p.first + m] * s;
+      ys[tb.entry[p.first + m] * kTile + c] += tb.weight[tb.slot[p.first + m]] * s;
     }
     __syncthreads();
   };
-  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close);
+  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close, [] {
+    pdl_wait();
+    pdl_release();
+  });
   cl.sync();
   // the cluster's CTAs finish the entries b mod 8 == rank
   for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) {
@@ -837,9 +906,10 @@ static aal_status launch(void (*k)(A...), dim3 grid, int threads, size_t smem, i
 template <typename T, int VEC, int TB>
 static aal_status run_router(const RouterArgs& a, cudaStream_t s) {
   const size_t ds = (a.D + kRouterCtas - 1) / kRouterCtas;
-  size_t red = (size_t)TB * VEC * kRouterThreads;
-  if (red < (size_t)a.E) red = a.E;  // it holds an entry's logits afterwards
-  const size_t smem = ((size_t)TB * a.E + red + TB * ds) * sizeof(double);
+  // an entry's logits and their keys take the place of the products afterwards
+  size_t red = (size_t)TB * VEC * kRouterThreads + TB * ds;
+  if (red < 2 * (size_t)a.E) red = 2 * (size_t)a.E;
+  const size_t smem = ((size_t)TB * a.E + red) * sizeof(double);
   if (smem > 200 * 1024) return AAL_ERR_UNSUPPORTED;
   return launch(k_moe_router<T, VEC, TB>, dim3((unsigned)((a.B + TB - 1) / TB * kRouterCtas)), kRouterThreads, smem, 0,
                 s, a);
@@ -878,9 +948,8 @@ static aal_status run_up(ExpertArgs a, size_t tables, cudaStream_t s) {
   a.by_tiles = tc::make_fastdiv((uint32_t)a.tiles);
   a.by_ntile = tc::make_fastdiv((uint32_t)a.ntile);
   // clusters for the pieces left over, while every warp of one keeps two steps
-  // (one step a warp: a token's 16-step pieces end no sooner)
   const int steps = (a.q < 2 ? 1 : 2) * (bi >> 4);
-  const int z = steps >= 32 ? 4 : steps >= 16 ? 2 : 1;
+  const int z = steps >= 32 ? 4 : 1;
   a.zsplit = z;
   const int used = a.B * a.k < a.E ? a.B * a.k : a.E;
   const long long pieces = (long long)a.ntile * used * z, room = 2LL * sms / z * z;

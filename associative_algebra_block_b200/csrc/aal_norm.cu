@@ -956,7 +956,7 @@ static Plan plan(long long d, int es, bool aligned, int arrays, int pes) {
     constexpr size_t kSm = 226 * 1024;  // of 227 KB; the static arrays take the rest
     p.gamma = arrays == 3 && !p.elem ? (size_t)d * pes : 0;
     const bool bwd = arrays == 3;
-    const int most = p.threads <= 128 ? (bwd ? 4 : 8) : (bwd ? 2 : 4);
+    const int most = p.threads <= 128 ? (bwd ? 8 : 16) : (bwd ? 2 : 4);
     int want = p.block ? (bwd ? 640 : 1024) / p.threads : 2;
     want = want < 1 ? 1 : want > most ? most : want;
     for (p.per_sm = want; p.per_sm > 1; --p.per_sm)
