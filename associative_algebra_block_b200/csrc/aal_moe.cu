@@ -366,7 +366,7 @@ __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& t
     const int e = tb.id[s], b = (int)tc::fdiv((uint32_t)s, a.by_k);
     if (e >= 0) {
       atomicOr(&tb.who[e * W + (b >> 5)], 1u << (b & 31));
-      atomicOr(&tb.tmask[e], 1u << tb.type[b]);
+      atomicOr(&tb.tmask[e], 1u << (tb.type[b] & 31));  // (read where q <= 32)
     }
   }
   __syncthreads();
@@ -555,14 +555,13 @@ struct Sums {
   }
 };
 
-// The loop both expert kernels share: ``open(i, walk)`` describes piece i of
-// this CTA for the calling warp, ``steps(i)`` is that warp's number of steps of
-// it, and ``close(i)`` runs after its sums are in red[warp] (no barrier yet).
-// All warps of the CTA close every piece.  ``ready`` is called once, before the
-// first input is read and after the first steps' weights are on their way.
+// The loop both expert kernels share: ``open(i, walk)`` describes the warp's
+// piece i, ``steps(i)`` is its number of steps, and ``close(i, sums)`` takes its
+// products.  ``ready`` is called once, before the first input is read and after
+// the first steps' weights are on their way.
 template <int NT, int S, typename Open, typename Steps, typename Close, typename Ready>
-__device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, int law, int pieces, Open open,
-                                           Steps steps, Close close, Ready ready) {
+__device__ __forceinline__ void run_pieces(unsigned char* ring_mem, int law, int pieces, Open open, Steps steps,
+                                           Close close, Ready ready) {
   Ring<NT, S> ring(ring_mem);
   Walk<NT> walk;
   walk.left = 0;
@@ -592,7 +591,6 @@ __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, 
     copy_commit();  // empty once the work has run out, so that the waits still count
   };
   for (int i = 0; i < S - 1; ++i) produce(false);
-  float* mine = red + (threadIdx.x >> 5) * Sums<NT>::kFloats;
   for (int i = 0; i < pieces; ++i) {
     float acc[4][NT][4] = {};
     for (int n = steps(i); n > 0; --n) {
@@ -601,8 +599,7 @@ __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, float* red, 
       ring.multiply(acc);
       produce(true);       // into the slot read in the round before
     }
-    Sums<NT>::put(mine, acc);
-    close(i);
+    close(i, acc);
   }
   copy_wait<0>();
 }
@@ -672,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
     const int p = piece(i, kg, c0);
     return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first(i), stride(i));
   };
-  auto close = [&](int i) {
+  auto close = [&](int i, const float (&acc)[4][NT][4]) {
+    Sums<NT>::put(red + warp * kRed, acc);
     const bool shared = i >= whole;
     if (shared) cl.sync();
     else __syncthreads();
@@ -696,26 +694,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
     if (shared) cl.sync();
     else __syncthreads();
   };
-  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close, [] {});
+  run_pieces<NT, S>(ring_mem, a.law, pieces, open, steps, close, [] {});
 }
 
-// 64 columns of y a cluster.  Its CTAs take the passes in turn, add every
-// pass's weighted products to their sums in shared memory, and the cluster
-// adds the CTAs' sums in rank order with the residual.  The passes that are
-// left when there is no longer one for every CTA are split along K.
-constexpr int kDownCtas = 8;
+// 64 columns of y a cluster.  A unit of work is a pass, or one of its kparts
+// interleaved parts along K where there are few; the cluster's 64 warps take
+// units in turn, each from first weight row to last on its own, and add the
+// weighted products to their CTA's sums in shared memory one after another in
+// unit order, so results do not depend on timing.  Then the cluster adds the CTAs' sums in rank order with the
+// residual.  (With a unit to all of a CTA's warps, summed and handed over with
+// barriers, 64 entries under Q_16 took 55 us: two K steps a warp and unit.)
+constexpr int kDownCtas = 8, kDownWarps = kDownCtas * kWarps;
+constexpr int kYRow = kTile + 2;  // floats between entries' sums
+
+// The turn goes from warp w to warp w + 1 through named barrier w + 1 of the
+// two.  (A flag in shared memory needs a fence, and a fence waits for the
+// warp's copies in flight: 0.7 us a turn.)
+__device__ __forceinline__ void take_turn(int warp) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"((warp + kWarps - 1) % kWarps + 1) : "memory");
+}
+__device__ __forceinline__ void pass_turn(int warp) {
+  asm volatile("barrier.cta.arrive %0, 64;" ::"r"(warp + 1) : "memory");
+}
+
 template <int NT, int S>
 __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down(const ExpertArgs a) {
   extern __shared__ __align__(128) unsigned char mem[];
-  constexpr int kRed = Sums<NT>::kFloats;
-  unsigned char* ring_mem = mem;
-  float* red = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);
-  float* ys = red + kWarps * kRed;  // [B][64]
-  const Tables tb(reinterpret_cast<unsigned char*>(ys + a.B * kTile), a);
+  float* ys = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);  // [B][kYRow]
+  const Tables tb(reinterpret_cast<unsigned char*>(ys + (a.B * kYRow + 3) / 4 * 4), a);
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / kDownCtas);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) ys[i] = 0.f;
+  for (int i = threadIdx.x; i < a.B * kYRow; i += kThreads) ys[i] = 0.f;
   const int bi = a.F / a.q, bo = a.D / a.q, spg = bi >> 4;
   const int kg = tile / a.tiles, c0 = kg * bo + (tile - kg * a.tiles) * kTile;
   const int width = min(kTile, (kg + 1) * bo - c0);
@@ -724,17 +734,30 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
   // after its own wait for the router.  So the tables and the first weights
   // come in while k_moe_up still runs; only its h needs the wait.
   const int np = build_tables(a, tb, 8 * NT);
-  const int whole = np / kDownCtas, left = np - whole * kDownCtas;
-  const int z = left > 4 ? 1 : left > 2 ? 2 : left == 2 ? 4 : 8;  // CTAs that share a left-over pass
-  const int pieces = whole + (rank / z < left ? 1 : 0);
-  auto pass = [&](int i) { return i < whole ? i * kDownCtas + rank : whole * kDownCtas + rank / z; };
-  auto first = [&](int i) { return i < whole ? warp : rank % z * kWarps + warp; };
-  auto stride = [&](int i) { return i < whole ? kWarps : kWarps * z; };
+  // Parts a pass: the fewest K steps a warp takes, where adding a unit's
+  // products costs about as much as a step.
+  int kparts = 1;
+  {
+    const int steps = (a.q < 2 ? 1 : 2) * spg;
+    int best = INT_MAX;
+    for (int k = 1; k <= 16 && steps >= 2 * k; k *= 2) {
+      const int c = (np * k + kDownWarps - 1) / kDownWarps * (steps + k) * (16 / k);
+      if (c < best) {
+        best = c;
+        kparts = k;
+      }
+    }
+  }
+  const int shift = __ffs(kparts) - 1;
+  // unit u = i * 64 + warp * 8 + rank
+  const int units = np << shift, mine = warp * kDownCtas + rank;
+  const int pieces = mine < units ? (units - mine + kDownWarps - 1) / kDownWarps : 0;
   const int col = 8 * (lane & 7);
   const bool wide = col < width;
   const __nv_bfloat16* wbase = a.wd + (long long)(lane >> 3) * a.ldd + c0 + (wide ? col : 0);
   auto open = [&](int i, Walk<NT>& w) {
-    const Pass p = tb.pass[pass(i)];
+    const int u = i * kDownWarps + mine;
+    const Pass p = tb.pass[u >> shift];
     w.wsize = wide ? 16 : 0;
     w.ldw = a.ldd;
     w.w = wbase + (long long)p.expert * a.F * a.ldd;
@@ -746,26 +769,50 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
       w.type[nt] = tb.type[tb.entry[at]];
     }
     w.spg = spg;
-    w.stride = stride(i);
+    w.stride = kparts;
     w.kg = kg;
-    w.start(a.law, groups_of(a.law, a.q, p.types, kg), first(i));
+    w.start(a.law, groups_of(a.law, a.q, p.types, kg), u & (kparts - 1));
   };
   auto steps = [&](int i) {
-    return walk_steps(groups_of(a.law, a.q, tb.pass[pass(i)].types, kg), spg, first(i), stride(i));
+    const int u = i * kDownWarps + mine;
+    return walk_steps(groups_of(a.law, a.q, tb.pass[u >> shift].types, kg), spg, u & (kparts - 1), kparts);
   };
-  auto close = [&](int i) {
-    __syncthreads();
-    const Pass p = tb.pass[pass(i)];
-    for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
-      const int m = j / kTile, c = j % kTile, o = Sums<NT>::at(m, c);
-      float s = 0.f;
+  auto close = [&](int i, const float (&acc)[4][NT][4]) {
+    const Pass p = tb.pass[(i * kDownWarps + mine) >> shift];
+    const int g = lane >> 2, t = lane & 3;
+    float* y[NT][2];
+    float wt[NT][2];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += red[w * kRed + o];
-      ys[tb.entry[p.first + m] * kTile + c] += tb.weight[tb.slot[p.first + m]] * s;
-    }
-    __syncthreads();
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int n = nt * 8 + 2 * t + o, at = p.first + (n < p.n ? n : 0);
+        wt[nt][o] = tb.weight[tb.slot[at]];
+        y[nt][o] = ys + tb.entry[at] * kYRow + 8 * g;
+      }
+    if (i > 0 || warp > 0) take_turn(warp);
+    // all loads before the stores: the sums' round trip is what the next warp waits for
+    float2 v[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[nt][o][k] = *reinterpret_cast<const float2*>(y[nt][o] + 2 * k);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        if (nt * 8 + 2 * t + o < p.n) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float2*>(y[nt][o] + 2 * k) =
+                make_float2(fmaf(wt[nt][o], acc[k][nt][o], v[nt][o][k].x), fmaf(wt[nt][o], acc[k][nt][2 + o], v[nt][o][k].y));
+        }
+    // to the next unit of this CTA, if there is one
+    if ((warp + 1 < kWarps ? i * kDownWarps + mine + kDownCtas : (i + 1) * kDownWarps + rank) < units) pass_turn(warp);
   };
-  run_pieces<NT, S>(ring_mem, red, a.law, pieces, open, steps, close, [] {
+  run_pieces<NT, S>(mem, a.law, pieces, open, steps, close, [] {
     pdl_wait();
     pdl_release();
   });
@@ -776,100 +823,234 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
     if (b % kDownCtas != rank || c >= width || a.positions[b] < 0) continue;
     float s = a.r ? __bfloat162float(a.r[(long long)b * a.ldr + c0 + c]) : 0.f;
 #pragma unroll
-    for (int v = 0; v < kDownCtas; ++v) s += cl.map_shared_rank(ys, v)[i];
+    for (int v = 0; v < kDownCtas; ++v) s += cl.map_shared_rank(ys, v)[b * kYRow + c];
     a.y[(long long)b * a.ldy + c0 + c] = __float2bfloat16_rn(s);
   }
   cl.sync();  // the peers' sums have been read
 }
 
 // ---------------------------------------------------------- experts, any shape
-// 32 output columns a CTA, the K range dealt to its 8 warps.  One (entry,
-// choice) a CTA row for gate/up, one entry for down.
+// fp32, and widths off the matrix instruction's grid.  The pieces of work are
+// the same passes and tiles, 32 columns wide here: a lane takes VEC adjacent
+// columns (16 bytes of an aligned row, else one) and multiplies every weight
+// it loads with the pass's entries, whose inputs wait in shared memory, zeroed
+// where an entry's table row does not use the group.  A CTA's warps deal the
+// rows of the used groups out, kLoads loads a lane at a time so that as many
+// are in flight, and meet in shared memory.
+constexpr int kGenTile = 32, kGenEntries = 8, kGenRows = 512;
+
 template <typename T>
 struct GenArgs {
-  const int64_t* positions;
-  const int* ids;
-  const float* weights;
+  ExpertArgs e;  // (its matrices are not used: those below have their type)
   const T *x, *wg, *wu, *wd, *r;
   T *h, *y;
-  long long ldx, ldg, ldu, ldd, ldh, ldr, ldy;
-  int law, q, k, D, F;
+  tc::FastDiv by_bi;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_moe_up_general(const GenArgs<T> a) {
-  __shared__ float sg[8][33], su[8][33];
-  pdl_wait();
-  pdl_release();
-  const int s = (int)blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = a.ids[s];
-  if (e < 0) return;
-  const int b = s / a.k, t = (int)(a.positions[b] % a.q);
-  const int c = (int)blockIdx.x * 32 + lane;
-  const int bi = a.D / a.q, bo = a.F / a.q;
-  float g = 0.f, u = 0.f;
-  if (c < a.F) {
-    int m[4];
-    const int n = table_members(a.law, a.q, t, c / bo, m);
-    for (int i = 0; i < n; ++i) {
-      const T* x = a.x + (long long)b * a.ldx + (long long)m[i] * bi;
-      const T* wg = a.wg + ((long long)e * a.D + (long long)m[i] * bi) * a.ldg + c;
-      const T* wu = a.wu + ((long long)e * a.D + (long long)m[i] * bi) * a.ldu + c;
-#pragma unroll 8
-      for (int j = warp; j < bi; j += 8) {
-        const float xv = ld_elem(x + j);
-        g = fmaf(xv, ld_elem(wg + (long long)j * a.ldg), g);
-        u = fmaf(xv, ld_elem(wu + (long long)j * a.ldu), u);
-      }
+// The groups that output group kg needs for a pass's entries (at most
+// kGenEntries + 1 under Q_q, 4 under Q2 x Q2); warp 0 lists them.
+__device__ __forceinline__ int list_groups(const ExpertArgs& a, const Tables& tb, const Pass& p, int kg, int* list) {
+  const int lane = threadIdx.x & 31;
+  if (a.q <= 32) {  // from the expert's types, which may be more than the pass's
+    const unsigned m = groups_of(a.law, a.q, p.types, kg);
+    if ((m >> lane) & 1u) list[__popc(m & ((1u << lane) - 1u))] = lane;
+    return __popc(m);
+  }
+  int n = 0;  // law Q_q: kg and the entries' types, each once
+  if (lane == 0) list[0] = kg;
+  n = 1;
+  for (int i = 0; i < p.n; ++i) {
+    const int t = tb.type[tb.entry[p.first + i]];
+    bool seen = t == kg;
+    for (int l = 0; l < i; ++l) seen |= tb.type[tb.entry[p.first + l]] == t;
+    if (!seen) {
+      if (lane == 0) list[n] = t;
+      ++n;
     }
   }
-  sg[warp][lane] = g;
-  su[warp][lane] = u;
-  __syncthreads();
-  if (warp || c >= a.F) return;
-  g = u = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    g += sg[i][lane];
-    u += su[i][lane];
-  }
-  st_elem(a.h + (long long)s * a.ldh + c, g / (1.f + expf(-g)) * u);
+  return n;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_moe_down_general(const GenArgs<T> a) {
-  __shared__ float sy[8][33];
+struct GenShared {
+  float x[kGenRows][kGenEntries];
+  int row[kGenRows];
+  float part[kWarps][kGenEntries][kGenTile];
+  int groups[32];
+  int ngroups;
+};
+
+// This warp's products of one matrix (row 0 at ``w``, the lane's columns) with
+// a pass's entries, in sh.part[warp].  The used groups' rows part / parts of
+// the way through are dealt to ``warps`` warps, of which this is number ``wi``;
+// ``in`` gives the input row of the choice at a place.
+template <typename T, int VEC, typename In>
+__device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& tb, GenShared& sh, const Pass& p, int kg,
+                                             int bi, const T* w, long long ldw, bool on, int wi, int warps, int part,
+                                             int parts, In in) {
+  constexpr int kLoads = VEC == 1 ? 24 : 8;
+  constexpr int kLanes = kGenTile / VEC, kSub = 32 / kLanes;  // lanes a row, rows a load instruction
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes;
+  float acc[kGenEntries][VEC] = {};
+  __syncthreads();  // the shared arrays are free
+  if (warp == 0) {
+    const int n = list_groups(g.e, tb, p, kg, sh.groups);
+    if (lane == 0) sh.ngroups = n;
+  }
+  __syncthreads();
+  const int total = sh.ngroups * bi;
+  const int lo = (int)((long long)total * part / parts), hi = (int)((long long)total * (part + 1) / parts);
+  for (int r0 = lo; r0 < hi; r0 += kGenRows) {
+    const int n = min(kGenRows, hi - r0);
+    for (int r = threadIdx.x; r < n; r += kThreads) {
+      const int gi = (int)tc::fdiv((uint32_t)(r0 + r), g.by_bi);
+      const int grp = sh.groups[gi], k = grp * bi + (r0 + r - gi * bi);
+      sh.row[r] = k;
+      float v[kGenEntries];
+#pragma unroll
+      for (int i = 0; i < kGenEntries; ++i) {
+        const int at = p.first + (i < p.n ? i : 0);
+        v[i] = i < p.n && in_table(g.e.law, tb.type[tb.entry[at]], kg, grp) ? ld_elem(in(at) + k) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kGenEntries; i += 4)
+        *reinterpret_cast<float4*>(&sh.x[r][i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    __syncthreads();
+    for (int b = wi * kLoads * kSub; b < n; b += warps * kLoads * kSub) {
+      float v[kLoads][VEC];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = b + j * kSub + sub;
+        const T* src = w + (long long)sh.row[r < n ? r : 0] * ldw;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) v[j][c] = 0.f;
+        if (on && r < n) {
+          if constexpr (VEC == 1) {
+            v[j][0] = ld_elem(src);
+          } else {
+            static_assert(sizeof(T) * VEC == 16, "a 16-byte vector");
+            const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+            v[j][0] = f.x;
+            v[j][1] = f.y;
+            v[j][2] = f.z;
+            v[j][3] = f.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = b + j * kSub + sub;
+        const float* xr = sh.x[r < n ? r : 0];
+#pragma unroll
+        for (int i = 0; i < kGenEntries; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(xr + i);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            acc[i][c] = fmaf(v[j][c], f.x, acc[i][c]);
+            acc[i + 1][c] = fmaf(v[j][c], f.y, acc[i + 1][c]);
+            acc[i + 2][c] = fmaf(v[j][c], f.z, acc[i + 2][c]);
+            acc[i + 3][c] = fmaf(v[j][c], f.w, acc[i + 3][c]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kGenEntries; ++i)
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      float v = acc[i][c];
+      for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0) sh.part[warp][i][lane * VEC + c] = v;
+    }
+  __syncthreads();
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_moe_up_general(const GenArgs<T> g) {
+  extern __shared__ __align__(128) unsigned char mem[];
+  __shared__ __align__(16) GenShared sh;
+  const ExpertArgs& a = g.e;
+  const Tables tb(mem, a);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_release();
-  const int b = (int)blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long pos = a.positions[b];
-  if (pos < 0) return;
-  const int t = (int)(pos % a.q);
-  const int c = (int)blockIdx.x * 32 + lane;
-  const int bi = a.F / a.q, bo = a.D / a.q;
-  float y = 0.f;
-  if (c < a.D) {
-    int m[4];
-    const int n = table_members(a.law, a.q, t, c / bo, m);
-    for (int j = 0; j < a.k; ++j) {
-      const int s = b * a.k + j, e = a.ids[s];
-      float p = 0.f;
-      for (int i = 0; i < n; ++i) {
-        const T* h = a.h + (long long)s * a.ldh + (long long)m[i] * bi;
-        const T* wd = a.wd + ((long long)e * a.F + (long long)m[i] * bi) * a.ldd + c;
-#pragma unroll 8
-        for (int r = warp; r < bi; r += 8) p = fmaf(ld_elem(h + r), ld_elem(wd + (long long)r * a.ldd), p);
+  const int np = build_tables(a, tb, kGenEntries);
+  const int bi = a.D / a.q, bo = a.F / a.q;
+  const int total = np * a.ntile;
+  const bool up = warp >= kWarps / 2;
+  const long long ldw = up ? a.ldu : a.ldg;
+  for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    const int pi = (int)tc::fdiv((uint32_t)id, a.by_ntile), tile = id - pi * a.ntile;
+    const Pass p = tb.pass[pi];
+    const int kg = (int)tc::fdiv((uint32_t)tile, a.by_tiles);
+    const int in_group = (tile - kg * a.tiles) * kGenTile, col = lane % (kGenTile / VEC) * VEC;
+    const bool on = in_group + col < bo;
+    const T* w = (up ? g.wu : g.wg) + (long long)p.expert * a.D * ldw + kg * bo + in_group + (on ? col : 0);
+    gen_multiply<T, VEC>(g, tb, sh, p, kg, bi, w, ldw, on, warp % (kWarps / 2), kWarps / 2, 0, 1,
+                         [&](int at) { return g.x + (long long)tb.entry[at] * a.ldx; });
+    // warp i finishes entry i
+    if (warp < p.n && in_group + lane < bo) {
+      float gs = 0.f, us = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWarps / 2; ++v) {
+        gs += sh.part[v][warp][lane];
+        us += sh.part[v + kWarps / 2][warp][lane];
       }
-      y = fmaf(a.weights[s], p, y);
+      st_elem(g.h + (long long)tb.slot[p.first + warp] * a.ldh + kg * bo + in_group + lane, gs / (1.f + expf(-gs)) * us);
     }
   }
-  sy[warp][lane] = y;
-  __syncthreads();
-  if (warp || c >= a.D) return;
-  y = a.r ? ld_elem(a.r + (long long)b * a.ldr + c) : 0.f;
+}
+
+// 32 columns of y a cluster, as in k_moe_down: its CTAs take the passes in
+// turn, or split the rows of each where there are fewer passes than CTAs.
+template <typename T, int VEC>
+__global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down_general(const GenArgs<T> g) {
+  extern __shared__ __align__(128) unsigned char mem[];
+  __shared__ __align__(16) GenShared sh;
+  const ExpertArgs& a = g.e;
+  float* ys = reinterpret_cast<float*>(mem);  // [B][32]
+  const Tables tb(mem + (size_t)a.B * kGenTile * sizeof(float), a);
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / kDownCtas);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < a.B * kGenTile; i += kThreads) ys[i] = 0.f;
+  const int bi = a.F / a.q, bo = a.D / a.q;
+  const int kg = tile / a.tiles, in_group = (tile - kg * a.tiles) * kGenTile, col = lane % (kGenTile / VEC) * VEC;
+  const bool on = in_group + col < bo;
+  // (k_moe_up_general has waited for the router before it lets this kernel start)
+  const int np = build_tables(a, tb, kGenEntries);
+  pdl_wait();
+  pdl_release();
+  // the passes past the last full round are split along their rows, z ways
+  const int whole = np / kDownCtas, left = np - whole * kDownCtas;
+  const int z = left > 4 ? 1 : left > 2 ? 2 : left == 2 ? 4 : 8;
+  for (int i = 0; i < whole + (rank / z < left ? 1 : 0); ++i) {
+    const bool split = i >= whole;
+    const Pass p = tb.pass[split ? whole * kDownCtas + rank / z : i * kDownCtas + rank];
+    const T* w = g.wd + (long long)p.expert * a.F * a.ldd + kg * bo + in_group + (on ? col : 0);
+    gen_multiply<T, VEC>(g, tb, sh, p, kg, bi, w, a.ldd, on, warp, kWarps, split ? rank % z : 0, split ? z : 1,
+                         [&](int at) { return g.h + (long long)tb.slot[at] * a.ldh; });
+    if (warp < p.n) {
+      float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y += sy[i][lane];
-  st_elem(a.y + (long long)b * a.ldy + c, y);
+      for (int v = 0; v < kWarps; ++v) s += sh.part[v][warp][lane];
+      const int at = p.first + warp;
+      ys[tb.entry[at] * kGenTile + lane] += tb.weight[tb.slot[at]] * s;
+    }
+  }
+  cl.sync();
+  for (int i = threadIdx.x; i < a.B * kGenTile; i += kThreads) {
+    const int b = i / kGenTile, l = i % kGenTile;
+    if (b % kDownCtas != rank || in_group + l >= bo || a.positions[b] < 0) continue;
+    const long long c = kg * bo + in_group + l;
+    float s = g.r ? ld_elem(g.r + (long long)b * a.ldr + c) : 0.f;
+#pragma unroll
+    for (int v = 0; v < kDownCtas; ++v) s += cl.map_shared_rank(ys, v)[i];
+    st_elem(g.y + (long long)b * a.ldy + c, s);
+  }
+  cl.sync();  // the peers' sums have been read
 }
 
 // ------------------------------------------------------------------ launches
@@ -934,8 +1115,12 @@ static bool vec16(const aal_mat& m) {
 }
 
 template <int NT, int S>
-static size_t ring_bytes() {
+static size_t up_bytes() {
   return (size_t)kWarps * (S * Ring<NT, S>::kStep + Sums<NT>::kFloats * sizeof(float));
+}
+template <int NT, int S>
+static size_t down_bytes(int B) {
+  return (size_t)kWarps * S * Ring<NT, S>::kStep + (size_t)(B * kYRow + 3) / 4 * 4 * sizeof(float);
 }
 constexpr size_t kHalfSm = 113 * 1024;  // shared memory of a CTA that leaves room for a second one
 
@@ -954,7 +1139,7 @@ static aal_status run_up(ExpertArgs a, size_t tables, cudaStream_t s) {
   const int used = a.B * a.k < a.E ? a.B * a.k : a.E;
   const long long pieces = (long long)a.ntile * used * z, room = 2LL * sms / z * z;
   return timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up<NT, S>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, ring_bytes<NT, S>() + tables,
+    return launch(k_moe_up<NT, S>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, up_bytes<NT, S>() + tables,
                   z > 1 ? z : 0, s, a);
   });
 }
@@ -965,7 +1150,7 @@ static aal_status run_down(ExpertArgs a, size_t tables, cudaStream_t s) {
   a.ntile = a.q * a.tiles;
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
     return launch(k_moe_down<NT, S>, dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
-                  ring_bytes<NT, S>() + (size_t)a.B * kTile * sizeof(float) + tables, 0, s, a);
+                  down_bytes<NT, S>(a.B) + tables, 0, s, a);
   });
 }
 // NT tiles of 8 entries a pass; a ring of four steps where two CTAs still
@@ -977,25 +1162,40 @@ static aal_status run_experts(ExpertArgs a, cudaStream_t s) {
   const int most = used + slots / (8 * NT);
   a.passes = slots < most ? slots : most;
   a.by_k = tc::make_fastdiv((uint32_t)a.k);
-  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k), sums = (size_t)a.B * kTile * sizeof(float);
-  const aal_status st = ring_bytes<NT, 4>() + tables <= kHalfSm ? run_up<NT, 4>(a, tables, s) : run_up<NT, 3>(a, tables, s);
+  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k);
+  const aal_status st = up_bytes<NT, 4>() + tables <= kHalfSm ? run_up<NT, 4>(a, tables, s) : run_up<NT, 3>(a, tables, s);
   if (st != AAL_OK) return st;
-  return ring_bytes<NT, 4>() + tables + sums <= kHalfSm ? run_down<NT, 4>(a, tables, s) : run_down<NT, 3>(a, tables, s);
+  return down_bytes<NT, 4>(a.B) + tables <= kHalfSm ? run_down<NT, 4>(a, tables, s) : run_down<NT, 3>(a, tables, s);
 }
 
-template <typename T>
-static aal_status run_general(int law, int q, const int64_t* positions, const aal_mat& x, const aal_mat& Wg,
-                              const aal_mat& Wu, const aal_mat& Wd, const aal_mat& R, const int* ids,
-                              const float* weights, int k, const aal_mat& h, const aal_mat& y, int B, int D, int F,
-                              cudaStream_t s) {
-  GenArgs<T> a = {positions, ids, weights, (const T*)x.ptr, (const T*)Wg.ptr, (const T*)Wu.ptr, (const T*)Wd.ptr,
-                  (const T*)R.ptr, (T*)h.ptr, (T*)y.ptr, x.ld, Wg.ld, Wu.ld, Wd.ld, h.ld, R.ld, y.ld, law, q, k, D, F};
+template <typename T, int VEC>
+static aal_status run_general(const ExpertArgs& e, const aal_mat& x, const aal_mat& Wg, const aal_mat& Wu,
+                              const aal_mat& Wd, const aal_mat& R, const aal_mat& h, const aal_mat& y, cudaStream_t s) {
+  GenArgs<T> g = {e, (const T*)x.ptr, (const T*)Wg.ptr, (const T*)Wu.ptr, (const T*)Wd.ptr, (const T*)R.ptr, (T*)h.ptr,
+                  (T*)y.ptr, {}};
+  ExpertArgs& a = g.e;
+  const int slots = a.B * a.k, used = slots < a.E ? slots : a.E, most = used + slots / kGenEntries;
+  a.passes = slots < most ? slots : most;
+  a.by_k = tc::make_fastdiv((uint32_t)a.k);
+  const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k);
+  const int sms = device_sms();
+  auto tiles = [&](int bo, int bi) {
+    a.tiles = (bo + kGenTile - 1) / kGenTile;
+    a.ntile = a.q * a.tiles;
+    a.by_tiles = tc::make_fastdiv((uint32_t)a.tiles);
+    a.by_ntile = tc::make_fastdiv((uint32_t)a.ntile);
+    g.by_bi = tc::make_fastdiv((uint32_t)bi);
+  };
+  tiles(a.F / a.q, a.D / a.q);
+  const long long pieces = (long long)a.ntile * a.passes, room = 2LL * sms;
   aal_status st = timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up_general<T>, dim3((unsigned)((F + 31) / 32), (unsigned)(B * k)), 256, 0, 0, s, a);
+    return launch(k_moe_up_general<T, VEC>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, tables, 0, s, g);
   });
   if (st != AAL_OK) return st;
+  tiles(a.D / a.q, a.F / a.q);
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch(k_moe_down_general<T>, dim3((unsigned)((D + 31) / 32), (unsigned)B), 256, 0, 0, s, a);
+    return launch(k_moe_down_general<T, VEC>, dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
+                  (size_t)a.B * kGenTile * sizeof(float) + tables, 0, s, g);
   });
 }
 
@@ -1031,6 +1231,7 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
                     moe::vec16(h);
   if (!fast && t_policy == AAL_PATH_TENSOR) return AAL_ERR_UNSUPPORTED;
   const size_t es = dt == AAL_F32 ? 4 : 2;
+  const bool wvec = moe::vec16(Wg) && moe::vec16(Wu) && moe::vec16(Wd) && (D / q) % 4 == 0 && (F / q) % 4 == 0;
   const bool rvec = moe::vec16(Wr) && (E * es) % 16 == 0;
   auto at = [&](const aal_mat& m, long long row) { return m.ptr ? (char*)m.ptr + row * m.ld * es : nullptr; };
   aal_status st = AAL_OK;
@@ -1046,25 +1247,20 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
       return rvec ? moe::run_router_tb<__nv_bfloat16, 8>(ra, s) : moe::run_router_tb<__nv_bfloat16, 1>(ra, s);
     });
     if (st != AAL_OK) return st;
-    if (fast) {
-      using bf = __nv_bfloat16;
-      moe::ExpertArgs a = {positions + b0, id, wt, (const bf*)at(x, b0), (const bf*)Wg.ptr, (const bf*)Wu.ptr,
-                           (const bf*)Wd.ptr, (const bf*)at(R, b0), (bf*)at(h, b0 * top_k), (bf*)at(y, b0), x.ld, Wg.ld,
-                           Wu.ld, Wd.ld, h.ld, R.ld, y.ld, law, q, nb, top_k, (int)E, (int)D, (int)F, 0,
-                           0, 0, 0, 0, {}, {}, {}};
-      // two tiles of entries a pass where experts get more than six on average
-      st = (long long)nb * top_k <= 6 * E ? moe::run_experts<1>(a, s) : moe::run_experts<2>(a, s);
-    } else {
-      aal_mat xs = x, Rs = R, hs = h, ys = y;
-      xs.ptr = at(x, b0);
-      Rs.ptr = at(R, b0);
-      hs.ptr = at(h, b0 * top_k);
-      ys.ptr = at(y, b0);
-      st = dt == AAL_F32 ? moe::run_general<float>(law, q, positions + b0, xs, Wg, Wu, Wd, Rs, id, wt, top_k, hs, ys,
-                                                   nb, (int)D, (int)F, s)
-                         : moe::run_general<__nv_bfloat16>(law, q, positions + b0, xs, Wg, Wu, Wd, Rs, id, wt, top_k,
-                                                           hs, ys, nb, (int)D, (int)F, s);
-    }
+    using bf = __nv_bfloat16;
+    aal_mat xs = x, Rs = R, hs = h, ys = y;
+    xs.ptr = at(x, b0);
+    Rs.ptr = at(R, b0);
+    hs.ptr = at(h, b0 * top_k);
+    ys.ptr = at(y, b0);
+    moe::ExpertArgs a = {positions + b0, id, wt, (const bf*)xs.ptr, (const bf*)Wg.ptr, (const bf*)Wu.ptr,
+                         (const bf*)Wd.ptr, (const bf*)Rs.ptr, (bf*)hs.ptr, (bf*)ys.ptr, x.ld, Wg.ld, Wu.ld, Wd.ld, h.ld,
+                         R.ld, y.ld, law, q, nb, top_k, (int)E, (int)D, (int)F, 0, 0, 0, 0, {}, {}, {}};
+    // two tiles of entries a pass where experts get more than six on average
+    if (fast) st = (long long)nb * top_k <= 6 * E ? moe::run_experts<1>(a, s) : moe::run_experts<2>(a, s);
+    else if (dt == AAL_F32 && wvec) st = moe::run_general<float, 4>(a, xs, Wg, Wu, Wd, Rs, hs, ys, s);
+    else if (dt == AAL_F32) st = moe::run_general<float, 1>(a, xs, Wg, Wu, Wd, Rs, hs, ys, s);
+    else st = moe::run_general<bf, 1>(a, xs, Wg, Wu, Wd, Rs, hs, ys, s);
   }
   if (st == AAL_OK) note_path(fast ? AAL_PATH_DECODE : AAL_PATH_GENERAL);
   return st;
