@@ -8,7 +8,7 @@
 //
 // with every "*" row t = position mod q of the table.  Three launches chained
 // by programmatic dependent launch:
-//   k_moe_router   a cluster an entry (or four): logits, top-k, weights
+//   k_moe_router   a cluster an entry (or two): logits, top-k, weights
 //   k_moe_up       gate, up and SiLU of one expert's 64 columns a CTA
 //   k_moe_down     64 columns of y a cluster, its CTAs dealing the experts out
 // The experts' weights are the work: each weight block that some entry needs
@@ -1095,12 +1095,14 @@ static aal_status run_router(const RouterArgs& a, cudaStream_t s) {
   return launch(k_moe_router<T, VEC, TB>, dim3((unsigned)((a.B + TB - 1) / TB * kRouterCtas)), kRouterThreads, smem, 0,
                 s, a);
 }
-// Four entries a cluster share its weight loads and conversions; one entry a
-// cluster leaves more SMs to few entries, and serves what does not fit.
+// Two entries a cluster share its weight loads and conversions (four need more
+// registers than the loads in flight leave: 25 against 17 us at 64 entries);
+// one entry a cluster leaves more SMs to few entries, and serves what does not
+// fit.
 template <typename T, int VEC>
 static aal_status run_router_tb(const RouterArgs& a, cudaStream_t s) {
   if (a.B > 16) {
-    const aal_status st = run_router<T, VEC, 4>(a, s);
+    const aal_status st = run_router<T, VEC, 2>(a, s);
     if (st != AAL_ERR_UNSUPPORTED) return st;
   }
   return run_router<T, VEC, 1>(a, s);
