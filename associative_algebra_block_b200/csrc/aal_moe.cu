@@ -1054,35 +1054,7 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------------------------ launches
-// A launch that may start while the stream's previous kernel runs (the kernels
-// wait for it before they touch global memory); ``cluster`` > 0 sets a cluster
-// size at launch.
-template <typename... A>
-static aal_status launch(void (*k)(A...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args) {
-  if (smem > 32 * 1024 &&  // the static arrays count too
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return AAL_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cluster > 0) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
-  note_launch();
-  return cuda_status(e);
-}
+using norm::launch_pdl;
 
 template <typename T, int VEC, int TB>
 static aal_status run_router(const RouterArgs& a, cudaStream_t s) {
@@ -1092,8 +1064,8 @@ static aal_status run_router(const RouterArgs& a, cudaStream_t s) {
   if (red < 2 * (size_t)a.E) red = 2 * (size_t)a.E;
   const size_t smem = ((size_t)TB * a.E + red) * sizeof(double);
   if (smem > 200 * 1024) return AAL_ERR_UNSUPPORTED;
-  return launch(k_moe_router<T, VEC, TB>, dim3((unsigned)((a.B + TB - 1) / TB * kRouterCtas)), kRouterThreads, smem, 0,
-                s, a);
+  return launch_pdl<k_moe_router<T, VEC, TB>>(dim3((unsigned)((a.B + TB - 1) / TB * kRouterCtas)), kRouterThreads, smem,
+                                              0, s, a);
 }
 // Two entries a cluster share its weight loads and conversions (four need more
 // registers than the loads in flight leave: 25 against 17 us at 64 entries);
@@ -1141,7 +1113,7 @@ static aal_status run_up(ExpertArgs a, size_t tables, cudaStream_t s) {
   const int used = a.B * a.k < a.E ? a.B * a.k : a.E;
   const long long pieces = (long long)a.ntile * used * z, room = 2LL * sms / z * z;
   return timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up<NT, S>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, up_bytes<NT, S>() + tables,
+    return launch_pdl<k_moe_up<NT, S>>(dim3((unsigned)(pieces < room ? pieces : room)), kThreads, up_bytes<NT, S>() + tables,
                   z > 1 ? z : 0, s, a);
   });
 }
@@ -1151,7 +1123,7 @@ static aal_status run_down(ExpertArgs a, size_t tables, cudaStream_t s) {
   a.tiles = (bo + kTile - 1) / kTile;
   a.ntile = a.q * a.tiles;
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch(k_moe_down<NT, S>, dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
+    return launch_pdl<k_moe_down<NT, S>>(dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
                   down_bytes<NT, S>(a.B) + tables, 0, s, a);
   });
 }
@@ -1191,12 +1163,12 @@ static aal_status run_general(const ExpertArgs& e, const aal_mat& x, const aal_m
   tiles(a.F / a.q, a.D / a.q);
   const long long pieces = (long long)a.ntile * a.passes, room = 2LL * sms;
   aal_status st = timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch(k_moe_up_general<T, VEC>, dim3((unsigned)(pieces < room ? pieces : room)), kThreads, tables, 0, s, g);
+    return launch_pdl<k_moe_up_general<T, VEC>>(dim3((unsigned)(pieces < room ? pieces : room)), kThreads, tables, 0, s, g);
   });
   if (st != AAL_OK) return st;
   tiles(a.D / a.q, a.F / a.q);
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch(k_moe_down_general<T, VEC>, dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
+    return launch_pdl<k_moe_down_general<T, VEC>>(dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
                   (size_t)a.B * kGenTile * sizeof(float) + tables, 0, s, g);
   });
 }

@@ -18,6 +18,7 @@
 
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 namespace aal {
@@ -987,22 +988,55 @@ static bool rows_aligned(const aal_mat& m) {
   return !m.ptr || (((uintptr_t)m.ptr % 16) == 0 && (m.rows <= 1 || (m.ld * es) % 16 == 0));
 }
 
-template <typename... A>
-static aal_status launch_pdl(void (*k)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  if (smem > 32 * 1024 &&  // the static arrays count too
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return AAL_ERR_CUDA;
+// Raises kernel K's limit of dynamic shared memory to ``bytes`` on the current
+// device, once (the driver call costs as much as a short kernel).
+template <auto K>
+static cudaError_t allow_shared(size_t bytes) {
+  constexpr int kDevices = 64;
+  static std::atomic<size_t> allowed[kDevices];
+  if (bytes <= 32 * 1024) return cudaSuccess;  // (the static arrays count too)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<size_t>* a = dev >= 0 && dev < kDevices ? &allowed[dev] : nullptr;
+  if (a && a->load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  // two threads may come here together: the limit only ever grows
+  int most = 0;
+  e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  cudaFuncAttributes f;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&f, K);
+  if (e != cudaSuccess) return e;
+  const size_t limit = (size_t)most - f.sharedSizeBytes;
+  if (bytes > limit) return cudaErrorInvalidValue;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+  if (e == cudaSuccess && a) a->store(limit, std::memory_order_relaxed);
+  return e;
+}
+
+// A launch that may start while the stream's previous kernel still runs (the
+// kernels wait for it before they touch what it writes); ``cluster`` > 0 sets a
+// cluster size at launch.
+template <auto K, typename... A>
+static aal_status launch_pdl(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args) {
+  if (allow_shared<K>(smem) != cudaSuccess) return AAL_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  if (cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, K, args...);
   note_launch();
   return cuda_status(e);
 }
@@ -1052,13 +1086,13 @@ struct FwdLaunch {
   aal_status run() {
     a.ring = p.stages;
     a.lpr = p.lpr;
-    return launch_pdl(k_ln_fwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>, dim3((unsigned)grid_of(p, a.rows)), p.threads, p.bytes, s,
-                      a);
+    return launch_pdl<k_ln_fwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>>(dim3((unsigned)grid_of(p, a.rows)), p.threads, p.bytes, 0,
+                                                                       s, a);
   }
 };
 template <typename T, typename TP>
 static aal_status run_fwd(const FwdArgs& a, const Plan& p, cudaStream_t s) {
-  if (p.wide) return launch_pdl(k_ln_fwd_wide<T, TP>, dim3((unsigned)grid_of(p, a.rows)), p.threads, 0, s, a);
+  if (p.wide) return launch_pdl<k_ln_fwd_wide<T, TP>>(dim3((unsigned)grid_of(p, a.rows)), p.threads, 0, 0, s, a);
   return with_shape<T, false>(p, FwdLaunch<T, TP>{a, p, s});
 }
 
@@ -1072,8 +1106,8 @@ struct BwdLaunch {
     a.ring = p.stages;
     a.lpr = p.lpr;
     a.ring_bytes = (uint32_t)p.bytes;
-    return launch_pdl(k_ln_bwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>, dim3((unsigned)grid_of(p, a.rows)), p.threads,
-                      p.bytes + p.gamma, s, a);
+    return launch_pdl<k_ln_bwd<T, TP, NV, TPR, SUB, ELEM, MAXT, MINB>>(dim3((unsigned)grid_of(p, a.rows)), p.threads,
+                                                                       p.bytes + p.gamma, 0, s, a);
   }
 };
 
@@ -1175,18 +1209,18 @@ aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const
   const aal_status st = timed(AAL_KERNEL_NORM_BWD, s, [&] {
     aal_status e = AAL_OK;
     if (cols && M > 0 && !parts) {  // first: dX may be written over X, dY or dR
-      e = dt == AAL_F32 ? norm::launch_pdl(norm::k_ln_bwd_cols<float>, dim3(gx), 1024, 0, s, a, dgamma.ptr, dbeta.ptr,
-                                           pf32, (int)accumulate)
-                        : norm::launch_pdl(norm::k_ln_bwd_cols<__nv_bfloat16>, dim3(gx), 1024, 0, s, a, dgamma.ptr,
-                                           dbeta.ptr, pf32, (int)accumulate);
+      e = dt == AAL_F32 ? norm::launch_pdl<norm::k_ln_bwd_cols<float>>(dim3(gx), 1024, 0, 0, s, a, dgamma.ptr, dbeta.ptr, pf32,
+                                                                    (int)accumulate)
+                        : norm::launch_pdl<norm::k_ln_bwd_cols<__nv_bfloat16>>(dim3(gx), 1024, 0, 0, s, a, dgamma.ptr, dbeta.ptr, pf32,
+                                                                            (int)accumulate);
     }
     a.part = parts ? ws : nullptr;
     if (e == AAL_OK && M > 0 && (dX.ptr || parts)) {
       if (p.wide) {  // (without column sums: parts is false)
         const dim3 g((unsigned)grid);
-        e = dt == AAL_F32     ? norm::launch_pdl(norm::k_ln_bwd_wide<float, float>, g, p.threads, 0, s, a)
-            : gdt == AAL_F32 ? norm::launch_pdl(norm::k_ln_bwd_wide<__nv_bfloat16, float>, g, p.threads, 0, s, a)
-                             : norm::launch_pdl(norm::k_ln_bwd_wide<__nv_bfloat16, __nv_bfloat16>, g, p.threads, 0, s, a);
+        e = dt == AAL_F32     ? norm::launch_pdl<norm::k_ln_bwd_wide<float, float>>(g, p.threads, 0, 0, s, a)
+            : gdt == AAL_F32 ? norm::launch_pdl<norm::k_ln_bwd_wide<__nv_bfloat16, float>>(g, p.threads, 0, 0, s, a)
+                             : norm::launch_pdl<norm::k_ln_bwd_wide<__nv_bfloat16, __nv_bfloat16>>(g, p.threads, 0, 0, s, a);
       } else if (dt == AAL_F32) {
         e = norm::with_shape<float, true>(p, norm::BwdLaunch<float, float>{a, p, s});
       } else if (gdt == AAL_F32) {
@@ -1196,7 +1230,7 @@ aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const
       }
     }
     if (e == AAL_OK && cols && (parts || M == 0))
-      e = norm::launch_pdl(norm::k_ln_bwd_reduce, dim3(gx, 2), 32 * norm::kReduceWarps, 0, s, (const float*)ws,
+      e = norm::launch_pdl<norm::k_ln_bwd_reduce>(dim3(gx, 2), 32 * norm::kReduceWarps, 0, 0, s, (const float*)ws,
                            M == 0 ? 0 : grid, (long long)d, dgamma.ptr, dbeta.ptr, pf32, (int)accumulate);
     return e;
   });
