@@ -9,8 +9,8 @@
 // with every "*" row t = position mod q of the table.  Three launches chained
 // by programmatic dependent launch:
 //   k_moe_router   a cluster an entry (or two): logits, top-k, weights
-//   k_moe_up       gate, up and SiLU of one expert's 64 columns a CTA
-//   k_moe_down     64 columns of y a cluster, its CTAs dealing the experts out
+//   k_moe_up       gate, up and SiLU of one expert's 64 columns a piece
+//   k_moe_down     64 columns of y a cluster, its warps dealing the experts out
 // The experts' weights are the work: each weight block that some entry needs
 // is read once for all entries that share the expert.
 #include "aal_internal.h"
@@ -698,13 +698,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
 }
 
 // 64 columns of y a cluster.  A unit of work is a pass, or one of its kparts
-// interleaved parts along K where there are few; the cluster's 64 warps take
+// interleaved parts along K where there are few; the cluster's warps take
 // units in turn, each from first weight row to last on its own, and add the
 // weighted products to their CTA's sums in shared memory one after another in
 // unit order, so results do not depend on timing.  Then the cluster adds the CTAs' sums in rank order with the
 // residual.  (With a unit to all of a CTA's warps, summed and handed over with
 // barriers, 64 entries under Q_16 took 55 us: two K steps a warp and unit.)
-constexpr int kDownCtas = 8, kDownWarps = kDownCtas * kWarps;
+constexpr int kDownCtas = 8;
 constexpr int kYRow = kTile + 2;  // floats between entries' sums
 
 // The turn goes from warp w to warp w + 1 through named barrier w + 1 of the
@@ -717,13 +717,16 @@ __device__ __forceinline__ void pass_turn(int warp) {
   asm volatile("barrier.cta.arrive %0, 64;" ::"r"(warp + 1) : "memory");
 }
 
-template <int NT, int S>
-__global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down(const ExpertArgs a) {
+// CL: CTAs of a cluster, 8, or 4 for little work, so that all of them find
+// room beside k_moe_up's and have their weights when it ends.
+template <int NT, int S, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads, 2) k_moe_down(const ExpertArgs a) {
+  constexpr int kUnits = CL * kWarps;  // units the cluster's warps take at once
   extern __shared__ __align__(128) unsigned char mem[];
   float* ys = reinterpret_cast<float*>(mem + kWarps * S * Ring<NT, S>::kStep);  // [B][kYRow]
   const Tables tb(reinterpret_cast<unsigned char*>(ys + (a.B * kYRow + 3) / 4 * 4), a);
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / kDownCtas);
+  const int rank = (int)cl.block_rank(), tile = (int)(blockIdx.x / CL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < a.B * kYRow; i += kThreads) ys[i] = 0.f;
   const int bi = a.F / a.q, bo = a.D / a.q, spg = bi >> 4;
@@ -741,7 +744,7 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
     const int steps = (a.q < 2 ? 1 : 2) * spg;
     int best = INT_MAX;
     for (int k = 1; k <= 16 && steps >= 2 * k; k *= 2) {
-      const int c = (np * k + kDownWarps - 1) / kDownWarps * (steps + k) * (16 / k);
+      const int c = (np * k + kUnits - 1) / kUnits * (steps + k) * (16 / k);
       if (c < best) {
         best = c;
         kparts = k;
@@ -749,14 +752,14 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
     }
   }
   const int shift = __ffs(kparts) - 1;
-  // unit u = i * 64 + warp * 8 + rank
-  const int units = np << shift, mine = warp * kDownCtas + rank;
-  const int pieces = mine < units ? (units - mine + kDownWarps - 1) / kDownWarps : 0;
+  // unit u = i * kUnits + warp * CL + rank
+  const int units = np << shift, mine = warp * CL + rank;
+  const int pieces = mine < units ? (units - mine + kUnits - 1) / kUnits : 0;
   const int col = 8 * (lane & 7);
   const bool wide = col < width;
   const __nv_bfloat16* wbase = a.wd + (long long)(lane >> 3) * a.ldd + c0 + (wide ? col : 0);
   auto open = [&](int i, Walk<NT>& w) {
-    const int u = i * kDownWarps + mine;
+    const int u = i * kUnits + mine;
     const Pass p = tb.pass[u >> shift];
     w.wsize = wide ? 16 : 0;
     w.ldw = a.ldd;
@@ -774,11 +777,11 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
     w.start(a.law, groups_of(a.law, a.q, p.types, kg), u & (kparts - 1));
   };
   auto steps = [&](int i) {
-    const int u = i * kDownWarps + mine;
+    const int u = i * kUnits + mine;
     return walk_steps(groups_of(a.law, a.q, tb.pass[u >> shift].types, kg), spg, u & (kparts - 1), kparts);
   };
   auto close = [&](int i, const float (&acc)[4][NT][4]) {
-    const Pass p = tb.pass[(i * kDownWarps + mine) >> shift];
+    const Pass p = tb.pass[(i * kUnits + mine) >> shift];
     const int g = lane >> 2, t = lane & 3;
     float* y[NT][2];
     float wt[NT][2];
@@ -810,20 +813,20 @@ __global__ void __cluster_dims__(kDownCtas, 1, 1) __launch_bounds__(kThreads, 2)
                 make_float2(fmaf(wt[nt][o], acc[k][nt][o], v[nt][o][k].x), fmaf(wt[nt][o], acc[k][nt][2 + o], v[nt][o][k].y));
         }
     // to the next unit of this CTA, if there is one
-    if ((warp + 1 < kWarps ? i * kDownWarps + mine + kDownCtas : (i + 1) * kDownWarps + rank) < units) pass_turn(warp);
+    if ((warp + 1 < kWarps ? i * kUnits + mine + CL : (i + 1) * kUnits + rank) < units) pass_turn(warp);
   };
   run_pieces<NT, S>(mem, a.law, pieces, open, steps, close, [] {
     pdl_wait();
     pdl_release();
   });
   cl.sync();
-  // the cluster's CTAs finish the entries b mod 8 == rank
+  // the cluster's CTAs finish the entries b mod CL == rank
   for (int i = threadIdx.x; i < a.B * kTile; i += kThreads) {
     const int b = i / kTile, c = i % kTile;
-    if (b % kDownCtas != rank || c >= width || a.positions[b] < 0) continue;
+    if (b % CL != rank || c >= width || a.positions[b] < 0) continue;
     float s = a.r ? __bfloat162float(a.r[(long long)b * a.ldr + c0 + c]) : 0.f;
 #pragma unroll
-    for (int v = 0; v < kDownCtas; ++v) s += cl.map_shared_rank(ys, v)[b * kYRow + c];
+    for (int v = 0; v < CL; ++v) s += cl.map_shared_rank(ys, v)[b * kYRow + c];
     a.y[(long long)b * a.ldy + c0 + c] = __float2bfloat16_rn(s);
   }
   cl.sync();  // the peers' sums have been read
@@ -1122,9 +1125,14 @@ static aal_status run_down(ExpertArgs a, size_t tables, cudaStream_t s) {
   const int bo = a.D / a.q;
   a.tiles = (bo + kTile - 1) / kTile;
   a.ntile = a.q * a.tiles;
+  const size_t smem = down_bytes<NT, S>(a.B) + tables;
+  // Clusters of 4 against 8: one token of 8 experts under Q_16 17.8 against
+  // 21.9 us a step (all three kernels), 16 entries of 4 experts 40.8 against
+  // 34.1 us.
+  const bool little = a.passes <= 16;
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
-    return launch_pdl<k_moe_down<NT, S>>(dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
-                  down_bytes<NT, S>(a.B) + tables, 0, s, a);
+    return little ? launch_pdl<k_moe_down<NT, S, 4>>(dim3((unsigned)(a.ntile * 4)), kThreads, smem, 0, s, a)
+                  : launch_pdl<k_moe_down<NT, S, 8>>(dim3((unsigned)(a.ntile * 8)), kThreads, smem, 0, s, a);
   });
 }
 // NT tiles of 8 entries a pass; a ring of four steps where two CTAs still

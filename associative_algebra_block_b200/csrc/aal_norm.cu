@@ -259,9 +259,12 @@ struct Group {
     return BLOCK ? block_sum2(a, 0.f, buf, turn).x : sum(a);
   }
   __device__ __forceinline__ float sum(float a) const {
-    if (!SUB) return warp_sum(a);
-    for (int o = tpr >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    return a;
+    if constexpr (SUB) {
+      for (int o = tpr >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      return a;
+    } else {
+      return warp_sum(a);
+    }
   }
 };
 
@@ -439,6 +442,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
       if (gr.lane < kEdgeThreads) {
         put_edge(m, x + row * a.ldx, ex);
         if (r) put_edge(mr, r + row * a.ldr, er);
+        tc::fence_async_smem();  // before the copy that refills the stage
       }
       edges(row + gr.step);
       m += (uint32_t)((uintptr_t)(x + row * a.ldx) & 15) + t * sizeof(T);
@@ -691,6 +695,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
         put_edge(m, x + row * a.ldx, ex);
         put_edge(my, dy + row * a.lddy, ey);
         if (dr) put_edge(mr, dr + row * a.lddr, er);
+        tc::fence_async_smem();  // before the copy that refills the stage
       }
       edges(row + gr.step);
       m += (uint32_t)((uintptr_t)(x + row * a.ldx) & 15) + t * sizeof(T);

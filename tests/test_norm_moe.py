@@ -360,6 +360,81 @@ def test_layer_norm_in_place_and_special_rows(cuda, d):
     assert torch.equal(Xb.nan_to_num(9), Yb.nan_to_num(9))
 
 
+# rows of several widths, many of them, back to back and odd in number: the
+# forms in which a warp takes several rows or a copy brings them at once
+@gpu
+@pytest.mark.parametrize("m,d,dtype", [(4097, 48, "bf16"), (1001, 96, "bf16"), (4099, 32, "f32"), (2051, 200, "bf16"),
+                                       (9001, 24, "f32"), (7, 128, "bf16"), (2501, 768, "bf16"), (1203, 2048, "bf16"),
+                                       (903, 333, "bf16"), (801, 1501, "f32"), (403, 5001, "bf16"), (300, 7000, "f32")])
+def test_layer_norm_many_contiguous_rows(cuda, m, d, dtype):
+    gen = torch.Generator().manual_seed(m + d)
+    X, R, dY = (torch.randn(m, d, generator=gen).to(TD[dtype]).cuda() for _ in range(3))
+    gamma, beta = (torch.randn(d, generator=gen).cuda() for _ in range(2))
+    Y, S, dX = (torch.full_like(X, float("nan")) for _ in range(3))
+    mean, rstd = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    aal.aal_layer_norm_fwd(X, gamma, beta, Y, R=R, S=S, mean=mean, rstd=rstd)
+    s = h64(X) + h64(R)
+    ref, mu, rs = oracle.layer_norm(s, h64(gamma), h64(beta))
+    e = 4 * _bound_terms(d)  # the mean, the variance (twice the mean's part) and the product
+    scale = np.abs(s).max(1)[:, None] * rs[:, None] * np.abs(h64(gamma)) + np.abs(h64(beta))
+    assert (np.abs(h64(Y) - ref) <= HALF[dtype] * np.abs(ref) + e * scale).all()
+    assert (np.abs(h64(S) - s) <= HALF[dtype] * np.abs(s) * 1.01).all()
+    dg, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    buf = torch.empty(aal.aal_layer_norm_bwd_workspace_size(m, d), dtype=torch.uint8, device="cuda")
+    aal.aal_set_workspace(buf)
+    try:
+        aal.aal_layer_norm_bwd(S, gamma, mean, rstd, dY, dX=dX, dgamma=dg, dbeta=db, dR=R)
+        again = torch.empty_like(dg)
+        aal.aal_layer_norm_bwd(S, gamma, mean, rstd, dY, dX=dX, dgamma=again, dbeta=db, dR=R)
+    finally:
+        aal.aal_set_workspace(None)
+    assert torch.equal(dg, again)  # the same sums in the same order
+    rx, rg, rb = oracle.layer_norm_bwd(h64(S), h64(gamma), h64(mean), h64(rstd), h64(dY))
+    xh = np.abs((h64(S) - h64(mean)[:, None]) * h64(rstd)[:, None])
+    g = np.abs(h64(dY) * h64(gamma))
+    mag = h64(rstd)[:, None] * (g + g.mean(1)[:, None] + (xh + np.abs(h64(mean) * h64(rstd))[:, None]) * (g * xh).mean(1)[:, None])
+    assert (np.abs(h64(dX) - rx - h64(R)) <= HALF[dtype] * np.abs(rx + h64(R)) + 4 * _bound_terms(d) * (mag + np.abs(h64(R)))).all()
+    n = (m / 32 + 700) * 2.0 ** -24
+    assert (np.abs(h64(dg) - rg) <= n * (np.abs(h64(dY)) * (xh + 1)).sum(0)).all()
+    assert (np.abs(h64(db) - rb) <= n * np.abs(h64(dY)).sum(0)).all()
+
+
+# every matrix at an alignment and a stride of its own
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [5, 64, 700, 1500])
+def test_layer_norm_mixed_alignments(cuda, d, dtype):
+    m = 37
+
+    def at(off, ld, seed):
+        big = torch.full((m, ld), 7.25, dtype=TD[dtype], device="cuda")
+        v = big[:, off:off + d]
+        v.copy_(torch.randn(m, d, generator=torch.Generator().manual_seed(seed)))
+        return v, big
+
+    X, _ = at(0, d + 8, 1)
+    R, _ = at(3, d + 5, 2)
+    S, Sb = at(1, d + 2, 3)
+    Y, Yb = at(7, d + 9, 4)
+    aal.aal_layer_norm_fwd(X, None, None, Y, R=R, S=S)
+    Xc, Rc, Yc, Sc = X.contiguous(), R.contiguous(), torch.empty(m, d, dtype=TD[dtype], device="cuda"), torch.empty(
+        m, d, dtype=TD[dtype], device="cuda")
+    ref, mu, rs = oracle.layer_norm(h64(Xc) + h64(Rc))
+    tol = HALF[dtype] * np.abs(ref) + 8 * _bound_terms(d) * (np.abs(h64(Xc) + h64(Rc)).max(1) * rs)[:, None]
+    assert (np.abs(h64(Y) - ref) <= tol).all()
+    assert (Yb[:, :7] == 7.25).all() and (Yb[:, 7 + d:] == 7.25).all() and (Sb[:, :1] == 7.25).all() and (Sb[:, 1 + d:] == 7.25).all()
+    aal.aal_layer_norm_fwd(Xc, None, None, Yc, R=Rc, S=Sc)
+    assert torch.equal(S, Sc)
+    dX, dXb = at(5, d + 11, 5)
+    mean, rstd = torch.from_numpy(mu).float().cuda(), torch.from_numpy(rs).float().cuda()
+    dg = torch.empty(d, device="cuda")
+    aal.aal_layer_norm_bwd(S, None, mean, rstd, X, dX=dX, dgamma=dg, dR=R)
+    rx, rg, _ = oracle.layer_norm_bwd(h64(S), None, h64(mean), h64(rstd), h64(X))
+    assert np.abs(h64(dX) - rx - h64(R)).max() <= HALF[dtype] * np.abs(rx + h64(R)).max() + 64 * _bound_terms(d)
+    assert np.abs(h64(dg) - rg).max() <= 200 * 2.0 ** -24 * np.abs(h64(X)).sum(0).max() * 4
+    assert (dXb[:, :5] == 7.25).all() and (dXb[:, 5 + d:] == 7.25).all()
+
+
 @gpu
 def test_layer_norm_offsets_past_32_bits(cuda):
     # rows 2^31 elements apart: the second row starts past a 32-bit offset
@@ -482,8 +557,16 @@ MOE = [
     (6, 8, 3, 128, 60, "Q2xQ2", 4, "f32", 4),
     (21, 7, 2, 45, 27, "Q", 3, "f32", 0),
     (2, 3, 1, 4096, 64, "Q", 32, "bf16", 0),
+    (1, 16, 8, 1024, 768, "Q", 8, "bf16", 0),      # a token: the small clusters
+    (32, 64, 8, 1024, 512, "Q", 1, "bf16", 0),     # pieces shared by clusters
+    (20, 4, 2, 768, 768, "Q", 1, "bf16", 0),       # two tiles of entries a pass
+    (128, 5, 3, 64, 96, "Q", 2, "bf16", 8),        # a full chain, several passes an expert
+    (70, 9, 4, 96, 64, "Q", 2, "f32", 0),
+    (3, 700, 9, 48, 80, "Q", 1, "f32", 0),         # experts beyond the counted ranking
+    (9, 6, 6, 300, 150, "Q", 150, "bf16", 0),      # groups of two and of one
+    (5, 12, 3, 202, 62, "Q", 2, "f32", 2),         # vectors off by two
     (1, 2, 2, 512, 512, "Q", 32, "bf16", 0),       # the largest q of the matrix path
-    (1, 2, 2, 4096, 4096, "Q", 256, "bf16", 0),
+    (1, 2, 2, 1024, 512, "Q", 256, "bf16", 0),
 ]
 
 
