@@ -6,13 +6,13 @@ leading dimension).  All arithmetic happens in the CUDA library; this module
 only checks that tensors are 2-D, row-major and on the GPU, and raises
 ``AalError`` for a non-OK status.  The library is loaded on first use and a
 missing ``libaal.so`` is an error (build it with ``__graft_entry__.build()``
-or ``python -m associative_algebra_block_b200.build``).
+or ``python -m associative_algebra_block_b200.build``).  The norm and expert
+calls go through a compiled marshaller (``_fastcall.so``, built with it).
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 import numpy as np
@@ -270,103 +270,33 @@ def aal_swiglu_decode_noalloc(law, q, positions, x, Wg, Wu, Wd, y, stream=None):
            "aal_swiglu_decode_noalloc")
 
 
-# Descriptors for the calls a decode step makes, whose kernels are short next
-# to the time Python takes to describe their arguments: one struct.pack writes
-# all of a call's aal_mat values into a per-thread buffer that ctypes views.
-# The checks are those of ``mat``; every tensor with entries must also be on
-# the current device, where the call launches.
-_DTYPE_CODE = {torch.bfloat16: AAL_BF16, torch.float32: AAL_F32}
-_NO_MAT = (0, AAL_BF16, 0, 0, 0)
-_MAT_FORMAT = "Qi4xqqq"  # ptr, dtype, rows, cols, ld
-_MAX_MATS = 8
+def _fast():
+    """The compiled marshaller of the norm and expert calls (csrc/fastcall.c):
+    a decode step's kernels are short next to the time Python takes to describe
+    eight tensors.  Its checks are those of ``mat`` and ``_index_vector``; every
+    tensor with entries must also be on the current device, where the call
+    launches."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        from . import _fastcall as f  # built beside libaal.so
+        address = (ctypes.cast(fn, ctypes.c_void_p).value
+                   for fn in (lib.aal_layer_norm_fwd, lib.aal_layer_norm_bwd, lib.aal_moe_decode))
+        f.setup(*address, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.cuda.current_device,
+                _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        _marshal = f
+    return _marshal
 
 
-class _Descriptors(threading.local):
-    def __init__(self):
-        size = struct.calcsize(_MAT_FORMAT)
-        assert size == ctypes.sizeof(AalMat)
-        self.buf = bytearray(size * _MAX_MATS)
-        self.mats = tuple(AalMat.from_buffer(self.buf, size * i) for i in range(_MAX_MATS))
-
-
-_descriptors = _Descriptors()
-_PACK = {n: struct.Struct(_MAT_FORMAT * n).pack_into for n in (6, 7, 8)}
-
-
-def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-
-
-def _wrong_device(t, dev):
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    raise ValueError(f"tensor is on CUDA device {t.get_device()}, the current one is {dev}")
-
-
-def _mat5(t, dev):
-    if t is None:
-        return _NO_MAT
-    code = _DTYPE_CODE.get(t.dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {t.dtype}")
-    try:
-        rows, cols = t.shape
-    except ValueError:
-        raise ValueError("expected a 2-D tensor") from None
-    if not rows or not cols:
-        return (0, code, rows, cols, cols)
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise ValueError("tensor must be row-major (unit column stride)")
-    if rows == 1:
-        ld = cols
-    elif ld < cols:
-        raise ValueError("the rows of a tensor must not overlap")
-    if t.get_device() != dev:
-        _wrong_device(t, dev)
-    return (t.data_ptr(), code, rows, cols, ld)
-
-
-def _vec5(t, dev, what):
-    """[1, d] view of a contiguous parameter vector."""
-    if t is None:
-        return _NO_MAT
-    if t.dim() != 1:
-        raise ValueError(f"{what} must be 1-D")
-    code = _DTYPE_CODE.get(t.dtype)
-    if code is None or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous, bf16 or fp32")
-    n = t.numel()
-    if n and t.get_device() != dev:
-        _wrong_device(t, dev)
-    return (t.data_ptr() if n else 0, code, 1, n, n)
-
-
-def _array(t, dev, dtype, n, what):
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with {n} entries")
-    if not n:
-        return None
-    if t.get_device() != dev:
-        _wrong_device(t, dev)
-    return t.data_ptr()
+_marshal = None
 
 
 def aal_layer_norm_fwd(X, gamma, beta, Y, eps=1e-5, R=None, S=None, mean=None, rstd=None, stream=None):
     """Y = layer norm of the rows of X (+ R) with gamma and beta [d] (either
     may be None); S receives the rounded sum, mean and rstd [rows] (fp32) the
     row statistics."""
-    dev, store = _device(), _descriptors
-    _PACK[6](store.buf, 0, *_mat5(X, dev), *_mat5(R, dev), *_vec5(gamma, dev, "gamma"), *_vec5(beta, dev, "beta"),
-             *_mat5(S, dev), *_mat5(Y, dev))
-    n = X.shape[0]
-    x, r, g, b, s, y, _, _ = store.mats
-    status = load().aal_layer_norm_fwd(x, r, g, b, eps, s, y, _array(mean, dev, torch.float32, n, "mean"),
-                                       _array(rstd, dev, torch.float32, n, "rstd"), _stream(stream))
+    status = (_marshal or _fast()).layer_norm_fwd(X, gamma, beta, Y, eps, R, S, mean, rstd,
+                                                   None if stream is None else _stream(stream))
     if status:
         raise AalError(status, "aal_layer_norm_fwd")
 
@@ -376,14 +306,8 @@ def aal_layer_norm_bwd(X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=Non
     """Gradients of aal_layer_norm_fwd; dR is added to dX.  dgamma and dbeta
     [d] come from the same pass when a workspace of
     aal_layer_norm_bwd_workspace_size(rows, d) bytes is set."""
-    dev, store = _device(), _descriptors
-    _PACK[7](store.buf, 0, *_mat5(X, dev), *_vec5(gamma, dev, "gamma"), *_mat5(dY, dev), *_mat5(dR, dev),
-             *_mat5(dX, dev), *_vec5(dgamma, dev, "dgamma"), *_vec5(dbeta, dev, "dbeta"))
-    n = X.shape[0]
-    x, g, dy, dr, dx, dg, db, _ = store.mats
-    status = load().aal_layer_norm_bwd(x, g, _array(mean, dev, torch.float32, n, "mean"),
-                                       _array(rstd, dev, torch.float32, n, "rstd"), dy, dr, dx, dg, db,
-                                       1 if accumulate else 0, _stream(stream))
+    status = (_marshal or _fast()).layer_norm_bwd(X, gamma, mean, rstd, dY, dX, dgamma, dbeta, dR, accumulate,
+                                                   None if stream is None else _stream(stream))
     if status:
         raise AalError(status, "aal_layer_norm_bwd")
 
@@ -400,17 +324,8 @@ def aal_moe_decode(law, q, positions, x, Wr, Wg, Wu, Wd, ids, weights, h, y, R=N
     """One decode step of a mixture of SwiGLU experts: Wr [D, E], the experts
     stacked by rows in Wg, Wu [E*D, F] and Wd [E*F, D]; ids (int32) and weights
     (fp32) [B, top_k] receive the choices, h [B*top_k, F] is workspace."""
-    dev, store = _device(), _descriptors
-    if ids.dim() != 2 or ids.shape[0] != x.shape[0]:
-        raise ValueError("ids must be [entries, top_k]")
-    n, k = ids.shape
-    pos = _array(positions, dev, torch.int64, n, "positions")
-    _PACK[8](store.buf, 0, *_mat5(x, dev), *_mat5(Wr, dev), *_mat5(Wg, dev), *_mat5(Wu, dev), *_mat5(Wd, dev),
-             *_mat5(R, dev), *_mat5(h, dev), *_mat5(y, dev))
-    mx, mr, mg, mu, md, mres, mh, my = store.mats
-    status = load().aal_moe_decode(_law(law), q, pos, mx, mr, mg, mu, md, mres, k, 1 if renormalize else 0,
-                                   _array(ids, dev, torch.int32, n * k, "ids"),
-                                   _array(weights, dev, torch.float32, n * k, "weights"), mh, my, _stream(stream))
+    status = (_marshal or _fast()).moe_decode(_law(law), q, positions, x, Wr, Wg, Wu, Wd, ids, weights, h, y, R,
+                                               renormalize, None if stream is None else _stream(stream))
     if status:
         raise AalError(status, "aal_moe_decode")
 

@@ -1,4 +1,5 @@
-"""Builds libaal.so in-tree with nvcc for sm_100a.
+"""Builds libaal.so in-tree with nvcc for sm_100a, and the binding's small
+argument marshaller (_fastcall.so) with the C compiler.
 
 Usage: ``python -m associative_algebra_block_b200.build`` (or
 ``__graft_entry__.build()``).  The library is one translation unit
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libaal.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -31,13 +34,13 @@ def nvcc_path() -> str:
 
 def sources():
     return sorted(os.path.join(SRC, f) for f in os.listdir(SRC)
-                  if f.endswith((".cu", ".h", ".cuh")))
+                  if f.endswith((".cu", ".h", ".cuh", ".c")))
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(FASTCALL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FASTCALL))
     deps = sources() + [os.path.join(INCLUDE, "aal.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -55,7 +58,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_fastcall()
     return LIB
+
+
+def build_fastcall() -> str:
+    """The binding's argument marshaller, a CPython extension in plain C."""
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler found")
+    tmp = FASTCALL + ".tmp"
+    subprocess.run([cc, "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall", "-I",
+                    sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", tmp, os.path.join(SRC, "fastcall.c")],
+                   check=True)
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
 
 
 if __name__ == "__main__":

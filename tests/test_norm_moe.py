@@ -749,3 +749,39 @@ def test_layer_norm_bwd_graphs_with_their_own_workspaces(cuda):
         assert torch.equal(p, r)
     _, rg, _ = oracle.layer_norm_bwd(h64(X), None, h64(mean), h64(rstd), h64(dY))
     assert oracle.rel_err(h64(outs[0][1]), rg) <= 1e-5
+
+
+def test_bindings_refuse_wrong_layouts(lib):
+    """The compiled marshaller's own checks, on host tensors (nothing launches)."""
+    bf = torch.bfloat16
+    e = torch.empty(0, 8, dtype=bf)
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        aal.aal_layer_norm_fwd(e.half(), None, None, e)
+    with pytest.raises(ValueError, match="2-D"):
+        aal.aal_layer_norm_fwd(torch.empty(0, dtype=bf), None, None, e)
+    with pytest.raises(ValueError, match="row-major"):
+        aal.aal_layer_norm_fwd(torch.empty(8, 4, dtype=bf).t(), None, None, e)
+    with pytest.raises(ValueError, match="overlap"):
+        aal.aal_layer_norm_fwd(torch.empty(1, 8, dtype=bf).expand(4, 8), None, None, e)
+    with pytest.raises(ValueError, match="contiguous"):
+        aal.aal_layer_norm_fwd(e, torch.empty(16, dtype=bf)[::2], None, e)
+    with pytest.raises(ValueError, match="contiguous, bf16 or fp32"):
+        aal.aal_layer_norm_fwd(e, torch.empty(8, dtype=torch.float16), None, e)
+    with pytest.raises(ValueError, match="3 entries|0 entries"):
+        aal.aal_layer_norm_fwd(e, None, None, e, rstd=torch.empty(3))
+    with pytest.raises((TypeError, AttributeError)):
+        aal.aal_layer_norm_fwd(3, None, None, e)
+    with pytest.raises(TypeError):
+        aal.aal_layer_norm_fwd(e, None, None, e, eps="x")
+    with pytest.raises(aal.AalError):
+        aal.aal_layer_norm_fwd(e, None, None, e, eps=-1.0)
+    w = torch.empty(8, 4, dtype=bf)
+    with pytest.raises(ValueError, match="ids"):
+        aal.aal_moe_decode("Q", 1, torch.empty(0, dtype=torch.int64), e, w, w, w, w, torch.empty(0, dtype=torch.int32),
+                           torch.empty(0), e, e)
+    with pytest.raises(ValueError, match="int64"):
+        aal.aal_moe_decode("Q", 1, torch.empty(0, dtype=torch.int32), e, e, e, e, e, torch.empty(0, 2, dtype=torch.int32),
+                           torch.empty(0, 2), e, e)
+    with pytest.raises(KeyError):
+        aal.aal_moe_decode("R", 1, torch.empty(0, dtype=torch.int64), e, e, e, e, e, torch.empty(0, 2, dtype=torch.int32),
+                           torch.empty(0, 2), e, e)
