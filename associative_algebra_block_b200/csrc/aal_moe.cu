@@ -28,7 +28,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 constexpr int kMaxTopK = 32;
-constexpr int kChunk = 128;  // entries of one chain of launches
+constexpr int kChunk = 128;   // entries of one chain of launches,
+constexpr int kSlots = 1024;  // and choices: what a CTA's tables hold beside its ring for 2048 experts
 
 // ------------------------------------------------------------------- router
 // A cluster of kRouterCtas CTAs takes TB entries: CTA r the input rows of
@@ -352,7 +353,7 @@ __device__ __forceinline__ int build_tables(const ExpertArgs& a, const Tables& t
   for (int s = threadIdx.x; s < n; s += blockDim.x) {
     const int e = __ldcg(a.ids + s);
     const float w = __ldcg(a.weights + s);
-    tb.id[s] = e;
+    tb.id[s] = e < a.E ? e : -1;
     tb.weight[s] = w;
   }
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
@@ -1085,6 +1086,7 @@ static aal_status run_router_tb(const RouterArgs& a, cudaStream_t s) {
 
 // The widest router the kernel holds in shared memory.
 constexpr int kMaxExperts = 2048;
+constexpr long long kMaxWidth = 1 << 20;  // of x and of h
 
 static bool vec16(const aal_mat& m) {
   const size_t es = m.dtype == AAL_F32 ? 4 : 2;
@@ -1198,13 +1200,15 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
     return AAL_ERR_UNSUPPORTED;
   const long long B = x.rows, D = x.cols, E = Wr.cols, F = Wg.cols;
   if (top_k < 1 || E < 1 || top_k > E) return AAL_ERR_INVALID_ARG;
+  // (pieces of a launch, 32 columns of 1024 passes at most, are counted in 32 bits)
+  if (top_k > moe::kMaxTopK || E > moe::kMaxExperts || D > moe::kMaxWidth || F > moe::kMaxWidth)
+    return AAL_ERR_UNSUPPORTED;
   if (Wr.rows != D || Wg.rows != E * D || Wu.rows != E * D || Wu.cols != F || Wd.rows != E * F || Wd.cols != D ||
       (R.ptr && (R.rows != B || R.cols != D)) || h.rows != B * top_k || h.cols != F || y.rows != B || y.cols != D)
     return AAL_ERR_INVALID_ARG;
   if (D % q || F % q) return AAL_ERR_INVALID_ARG;
   if (((uintptr_t)positions % 8) || ((uintptr_t)ids % 4) || ((uintptr_t)weights % 4)) return AAL_ERR_INVALID_ARG;
   if (B > 0 && (!positions || !ids || !weights)) return AAL_ERR_INVALID_ARG;
-  if (top_k > moe::kMaxTopK || E > moe::kMaxExperts || D > INT_MAX || F > INT_MAX) return AAL_ERR_UNSUPPORTED;
   note_path(0);
   if (B == 0 || D == 0 || F == 0) return AAL_OK;
   cudaStream_t s = (cudaStream_t)stream;
@@ -1217,8 +1221,9 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
   const bool rvec = moe::vec16(Wr) && (E * es) % 16 == 0;
   auto at = [&](const aal_mat& m, long long row) { return m.ptr ? (char*)m.ptr + row * m.ld * es : nullptr; };
   aal_status st = AAL_OK;
-  for (long long b0 = 0; b0 < B && st == AAL_OK; b0 += moe::kChunk) {
-    const int nb = (int)(B - b0 < moe::kChunk ? B - b0 : moe::kChunk);
+  const int chunk = moe::kSlots / top_k < moe::kChunk ? moe::kSlots / top_k : moe::kChunk;
+  for (long long b0 = 0; b0 < B && st == AAL_OK; b0 += chunk) {
+    const int nb = (int)(B - b0 < chunk ? B - b0 : chunk);
     int* id = ids + b0 * top_k;
     float* wt = weights + b0 * top_k;
     moe::RouterArgs ra = {at(x, b0), Wr.ptr, positions + b0, id, wt, x.ld, Wr.ld, nb, (int)D, (int)E, top_k,

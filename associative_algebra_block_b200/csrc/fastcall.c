@@ -182,6 +182,13 @@ static int get_array(call_ctx* c, PyObject* t, PyObject* dtype, long long n, con
   return n ? place(c, t, ptr) : 0;
 }
 
+/* An argument that may be left out must not pass for left out by being empty. */
+static int not_empty(PyObject* t, const aal_mat* m, const char* what) {
+  if (t == Py_None || m->ptr) return 0;
+  PyErr_Format(PyExc_ValueError, "%s has no entries: its shape must be that of the call", what);
+  return -1;
+}
+
 /* The stream handed in, or the current one of the call's device. */
 static int get_stream(const call_ctx* c, PyObject* given, void** out) {
   *out = NULL;
@@ -219,6 +226,9 @@ static PyObject* norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       get_array(&c, a[7], d_f32, X.rows, "mean", &mean) || get_array(&c, a[8], d_f32, X.rows, "rstd", &rstd) ||
       get_stream(&c, a[9], &stream))
     return NULL;
+  if (X.ptr && (not_empty(a[5], &R, "R") || not_empty(a[1], &g, "gamma") || not_empty(a[2], &b, "beta") ||
+                not_empty(a[6], &S, "S")))
+    return NULL;
   const double eps = PyFloat_AsDouble(a[4]);
   if (eps == -1.0 && PyErr_Occurred()) return NULL;
   return PyLong_FromLong(f_norm_fwd(X, R, g, b, (float)eps, S, Y, (float*)mean, (float*)rstd, stream));
@@ -236,6 +246,9 @@ static PyObject* norm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       get_vec(&c, a[7], "dbeta", &db) || get_array(&c, a[2], d_f32, X.rows, "mean", &mean) ||
       get_array(&c, a[3], d_f32, X.rows, "rstd", &rstd) || get_stream(&c, a[10], &stream))
     return NULL;
+  if (X.cols && (not_empty(a[1], &g, "gamma") || not_empty(a[6], &dg, "dgamma") || not_empty(a[7], &db, "dbeta")))
+    return NULL;
+  if (X.ptr && (not_empty(a[8], &dR, "dR") || not_empty(a[5], &dX, "dX"))) return NULL;
   return PyLong_FromLong(
       f_norm_bwd(X, g, (const float*)mean, (const float*)rstd, dY, dR, dX, dg, db, acc, stream));
 }
@@ -266,6 +279,7 @@ static PyObject* moe(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       get_mat(&c, a[11], &y) || get_array(&c, a[8], d_i32, rows * k, "ids", &ids) ||
       get_array(&c, a[9], d_f32, rows * k, "weights", &wt) || get_stream(&c, a[14], &stream))
     return NULL;
+  if (x.ptr && not_empty(a[12], &r, "R")) return NULL;
   return PyLong_FromLong(f_moe((int32_t)law, (int32_t)q, (const int64_t*)pos, x, wr, wg, wu, wd, r, (int32_t)k, renorm,
                                (int32_t*)ids, (float*)wt, h, y, stream));
 }

@@ -317,14 +317,17 @@ AAL_API int64_t aal_layer_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  *   order of falling logit, overwritten.  h [B k, F]: caller's workspace,
  *   overwritten with the activations of the choices.  y [B, D]: overwritten;
  *   it may be R or x itself.
- * Up to 128 entries take three chained launches.  bf16 calls with q <= 32,
- * D / q and F / q multiples of 16 and 16-byte aligned rows run on the tensor
- * cores (aal_last_path 3) and read each expert's weight blocks once for all
- * entries that chose it (once per 16 entries of one expert); there a block
- * that one entry of an expert uses also meets zeros from the expert's other
- * entries, so weights have to be finite.  Other calls take the general path.
+ * Up to min(128, 1024 / top_k) entries take three chained launches, more
+ * entries three for every so many.  bf16 calls with q <= 32, D / q and F / q
+ * multiples of 16 and 16-byte aligned rows run on the tensor cores
+ * (aal_last_path 3), others on the general path.  Either way a launch reads an
+ * expert's weight blocks once for every 8 (or 16) entries that chose it, and a
+ * block that one entry of an expert uses also meets zeros from the expert's
+ * other entries: its weights have to be finite.  Experts that no entry chose,
+ * and blocks that no entry of an expert uses, are not read.
  * Limits: top_k <= 32 and <= E, E <= 2048 (AAL_ERR_UNSUPPORTED above 32 and
- * 2048, AAL_ERR_INVALID_ARG above E).
+ * 2048, AAL_ERR_INVALID_ARG above E); D up to about 150,000 and F up to
+ * 1,048,576 (AAL_ERR_UNSUPPORTED above).
  * An entry with a negative position is skipped: its row of y is not written,
  * its ids are -1 and its weights 0, and the device status reports
  * AAL_ERR_DEVICE_BOUNDS.  An entry whose logits hold a NaN has k different

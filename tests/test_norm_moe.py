@@ -148,6 +148,8 @@ def test_moe_refusals(lib):
     assert call(wr=_m(FAKE, D, 2049), wg=_m(FAKE, 2049 * D, F), wu=_m(FAKE, 2049 * D, F), wd=_m(FAKE, 2049 * F, D)) == UNS
     assert call(wr=_m(FAKE, D, 64), wg=_m(FAKE, 64 * D, F), wu=_m(FAKE, 64 * D, F), wd=_m(FAKE, 64 * F, D), k=33,
                 h=_m(FAKE, B * 33, F)) == UNS
+    wide = 2 ** 20 + 2
+    assert call(wg=_m(FAKE, E * D, wide), wu=_m(FAKE, E * D, wide), wd=_m(FAKE, E * wide, D), h=_m(FAKE, B * k, wide)) == UNS
     # nothing to do: no entries
     assert call(pos=None, x=_m(None, 0, D), ids=None, w=None, h=_m(None, 0, F), y=_m(None, 0, D)) == aal.AAL_OK
 
@@ -161,6 +163,8 @@ def test_bindings_refuse_wrong_tensors(lib):
         aal.aal_layer_norm_fwd(e, torch.empty(0, 8), None, e)
     with pytest.raises(ValueError, match="float32"):
         aal.aal_layer_norm_fwd(e, None, None, e, mean=torch.empty(0, dtype=torch.float64))
+    with pytest.raises(ValueError, match="no entries"):  # empty is not left out
+        aal.aal_layer_norm_bwd(e, torch.empty(0), torch.empty(0), torch.empty(0), e)
     with pytest.raises(ValueError, match="entries"):
         aal.aal_layer_norm_bwd(e, None, torch.empty(3), torch.empty(0), e)
     pos = torch.zeros(4, dtype=torch.int64)
@@ -562,6 +566,9 @@ MOE = [
     (20, 4, 2, 768, 768, "Q", 1, "bf16", 0),       # two tiles of entries a pass
     (128, 5, 3, 64, 96, "Q", 2, "bf16", 8),        # a full chain, several passes an expert
     (70, 9, 4, 96, 64, "Q", 2, "f32", 0),
+    (75, 40, 31, 64, 32, "Q", 2, "bf16", 0),       # chains of 33 entries
+    (128, 2048, 8, 32, 16, "Q", 1, "bf16", 0),     # the largest tables
+    (128, 2048, 8, 32, 17, "Q", 1, "bf16", 0),
     (3, 700, 9, 48, 80, "Q", 1, "f32", 0),         # experts beyond the counted ranking
     (9, 6, 6, 300, 150, "Q", 150, "bf16", 0),      # groups of two and of one
     (5, 12, 3, 202, 62, "Q", 2, "f32", 2),         # vectors off by two
@@ -785,3 +792,66 @@ def test_bindings_refuse_wrong_layouts(lib):
     with pytest.raises(KeyError):
         aal.aal_moe_decode("R", 1, torch.empty(0, dtype=torch.int64), e, e, e, e, e, torch.empty(0, 2, dtype=torch.int32),
                            torch.empty(0, 2), e, e)
+
+
+@gpu
+def test_bindings_do_not_take_an_empty_tensor_for_one_left_out(cuda):
+    X, Y = (torch.ones(4, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    st = torch.ones(4, device="cuda")
+    none, flat = X[:0], X.reshape(-1)[:0]
+    for kw in (dict(R=none), dict(R=X, S=none)):
+        with pytest.raises(ValueError, match="no entries"):
+            aal.aal_layer_norm_fwd(X, None, None, Y, **kw)
+    for g, b in ((flat, None), (None, flat)):
+        with pytest.raises(ValueError, match="no entries"):
+            aal.aal_layer_norm_fwd(X, g, b, Y)
+    for kw in (dict(dX=none), dict(dX=Y, dR=none), dict(dgamma=flat), dict(dbeta=flat)):
+        with pytest.raises(ValueError, match="no entries"):
+            aal.aal_layer_norm_bwd(X, None, st, st, X, **kw)
+    m = Moe(2, 4, 2, 32, 32, "Q", 2, "bf16")
+    m.R = m.x[:0]
+    with pytest.raises(ValueError, match="no entries"):
+        m.run()
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+import associative_algebra_block_b200 as aal
+
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16() * 0.1
+X, big = r(64, 768), torch.randn(4, 8192, device="cuda")
+mean, rstd = torch.zeros(64, device="cuda"), torch.ones(64, device="cuda")
+D, F, E, k, B = 256, 128, 8, 2, 3
+pos, ids, w = torch.arange(B, device="cuda"), torch.empty(B, k, dtype=torch.int32, device="cuda"), torch.empty(B, k, device="cuda")
+x, Wr, Wg, Wu, Wd, h = r(B, D), r(D, E), r(E * D, F), r(E * D, F), r(E * F, D), r(B * k, F)
+Y, dX, bo, dg, y = torch.empty_like(X), torch.empty_like(X), torch.empty_like(big), torch.empty(768, device="cuda"), r(B, D)
+ws = torch.empty(aal.aal_layer_norm_bwd_workspace_size(64, 768), dtype=torch.uint8, device="cuda")
+aal.aal_set_workspace(ws)
+
+def calls():
+    aal.aal_layer_norm_fwd(X, None, None, Y, mean=mean, rstd=rstd)
+    aal.aal_layer_norm_fwd(big, None, None, bo)
+    aal.aal_layer_norm_bwd(X, None, mean, rstd, Y, dX=dX, dgamma=dg)
+    aal.aal_moe_decode("Q", 2, pos, x, Wr, Wg, Wu, Wd, ids, w, h, y)
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (Y, bo, dX, dg, y)]
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (Y, bo, dX, dg, y)))
+"""
+
+
+@gpu
+def test_the_first_calls_of_a_process_may_be_captured(cuda):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
