@@ -607,10 +607,9 @@ __device__ __forceinline__ void run_pieces(unsigned char* ring_mem, int law, int
 
 // h of the passes' 64-column tiles.  A piece is (pass, tile); warps 0-3 stream
 // the gate's weights, warps 4-7 the up projection's, every fourth step each.
-// The CTAs take whole pieces as long as there is one for every CTA; what is
-// left is shared by clusters of zsplit CTAs, which split K further and add
-// their parts in rank order through distributed shared memory (a last round
-// of whole pieces would leave most SMs idle).
+// Where the pieces leave SMs without one, a cluster of zsplit CTAs takes each:
+// they split K further and add their parts in rank order through distributed
+// shared memory.
 template <int NT, int S>
 __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
   extern __shared__ __align__(128) unsigned char mem[];
@@ -626,22 +625,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
   const int np = build_tables(a, tb, 8 * NT);
   const int bi = a.D / a.q, bo = a.F / a.q, spg = bi >> 4;
   const int total = np * a.ntile;
-  const int whole = z > 1 ? total / (int)gridDim.x : (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   const int team = (int)(blockIdx.x / z), teams = (int)(gridDim.x / z);
-  const int rest = z > 1 ? total - whole * (int)gridDim.x - team : 0;  // pieces left from this cluster's first on
-  const int pieces = whole + (rest > 0 ? (rest + teams - 1) / teams : 0);
+  const int pieces = team < total ? (total - team + teams - 1) / teams : 0;
   // piece i: its pass, output group and first column
   auto piece = [&](int i, int& kg, int& c0) {
-    const int id = i < whole ? (int)blockIdx.x + i * (int)gridDim.x
-                             : whole * (int)gridDim.x + team + (i - whole) * teams;
+    const int id = team + i * teams;
     const int p = (int)tc::fdiv((uint32_t)id, a.by_ntile), tile = id - p * a.ntile;
     kg = (int)tc::fdiv((uint32_t)tile, a.by_tiles);
     c0 = kg * bo + (tile - kg * a.tiles) * kTile;
     return p;
   };
-  const int w4 = warp & 3;
-  auto first = [&](int i) { return i < whole ? w4 : rank * 4 + w4; };
-  auto stride = [&](int i) { return i < whole ? 4 : 4 * z; };
+  const int first = rank * 4 + (warp & 3), stride = 4 * z;
   const long long ldw = warp >= 4 ? a.ldu : a.ldg;
   const __nv_bfloat16* wbase = (warp >= 4 ? a.wu : a.wg) + (long long)(lane >> 3) * ldw;
   auto open = [&](int i, Walk<NT>& w) {
@@ -661,29 +655,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
       w.type[nt] = tb.type[b];
     }
     w.spg = spg;
-    w.stride = stride(i);
+    w.stride = stride;
     w.kg = kg;
-    w.start(a.law, groups_of(a.law, a.q, p.types, kg), first(i));
+    w.start(a.law, groups_of(a.law, a.q, p.types, kg), first);
   };
   auto steps = [&](int i) {
     int kg, c0;
     const int p = piece(i, kg, c0);
-    return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first(i), stride(i));
+    return walk_steps(groups_of(a.law, a.q, tb.pass[p].types, kg), spg, first, stride);
   };
   auto close = [&](int i, const float (&acc)[4][NT][4]) {
     Sums<NT>::put(red + warp * kRed, acc);
-    const bool shared = i >= whole;
-    if (shared) cl.sync();
+    if (z > 1) cl.sync();
     else __syncthreads();
     int kg, c0;
     const Pass p = tb.pass[piece(i, kg, c0)];
     const int width = min(kTile, (kg + 1) * bo - c0);
     for (int j = threadIdx.x; j < p.n * kTile; j += kThreads) {
       const int m = j / kTile, c = j % kTile, o = Sums<NT>::at(m, c);
-      if (c >= width || (shared && m % z != rank)) continue;  // a cluster's CTAs finish every z-th entry
+      if (c >= width || (z > 1 && m % z != rank)) continue;  // a cluster's CTAs finish every z-th entry
       float g = 0.f, u = 0.f;
-      for (int v = 0; v < (shared ? z : 1); ++v) {
-        const float* from = shared ? cl.map_shared_rank(red, v) : red;
+      for (int v = 0; v < z; ++v) {
+        const float* from = z > 1 ? cl.map_shared_rank(red, v) : red;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           g += from[w * kRed + o];
@@ -692,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_up(const ExpertArgs a) {
       }
       a.h[(long long)tb.slot[p.first + m] * a.ldh + c0 + c] = __float2bfloat16_rn(g / (1.f + expf(-g)) * u);
     }
-    if (shared) cl.sync();
+    if (z > 1) cl.sync();
     else __syncthreads();
   };
   run_pieces<NT, S>(ring_mem, a.law, pieces, open, steps, close, [] {});
@@ -887,14 +880,17 @@ struct GenShared {
 // a pass's entries, in sh.part[warp].  The used groups' rows part / parts of
 // the way through are dealt to ``warps`` warps, of which this is number ``wi``;
 // ``in`` gives the input row of the choice at a place.
-template <typename T, int VEC, typename In>
-__device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& tb, GenShared& sh, const Pass& p, int kg,
+// NE: the most entries of the pass that are multiplied (the instructions are
+// what bounds this path: 27 entries of 64 experts, about two a pass, took 567
+// us a step with eight each).
+template <typename T, int VEC, int NE, typename In>
+__device__ __forceinline__ void gen_multiply_entries(const GenArgs<T>& g, const Tables& tb, GenShared& sh, const Pass& p, int kg,
                                              int bi, const T* w, long long ldw, bool on, int wi, int warps, int part,
                                              int parts, In in) {
   constexpr int kLoads = VEC == 1 ? 24 : 8;
   constexpr int kLanes = kGenTile / VEC, kSub = 32 / kLanes;  // lanes a row, rows a load instruction
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kLanes;
-  float acc[kGenEntries][VEC] = {};
+  float acc[NE][VEC] = {};
   __syncthreads();  // the shared arrays are free
   if (warp == 0) {
     const int n = list_groups(g.e, tb, p, kg, sh.groups);
@@ -909,15 +905,14 @@ __device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& 
       const int gi = (int)tc::fdiv((uint32_t)(r0 + r), g.by_bi);
       const int grp = sh.groups[gi], k = grp * bi + (r0 + r - gi * bi);
       sh.row[r] = k;
-      float v[kGenEntries];
+      float v[NE];
 #pragma unroll
-      for (int i = 0; i < kGenEntries; ++i) {
+      for (int i = 0; i < NE; ++i) {
         const int at = p.first + (i < p.n ? i : 0);
         v[i] = i < p.n && in_table(g.e.law, tb.type[tb.entry[at]], kg, grp) ? ld_elem(in(at) + k) : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < kGenEntries; i += 4)
-        *reinterpret_cast<float4*>(&sh.x[r][i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      for (int i = 0; i < NE; i += 2) *reinterpret_cast<float2*>(&sh.x[r][i]) = make_float2(v[i], v[i + 1]);
     }
     __syncthreads();
     for (int b = wi * kLoads * kSub; b < n; b += warps * kLoads * kSub) {
@@ -945,23 +940,31 @@ __device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& 
       for (int j = 0; j < kLoads; ++j) {
         const int r = b + j * kSub + sub;
         const float* xr = sh.x[r < n ? r : 0];
+        float xe[NE];
+        if constexpr (NE == 2) {
+          const float2 f = *reinterpret_cast<const float2*>(xr);
+          xe[0] = f.x;
+          xe[1] = f.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kGenEntries; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(xr + i);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            acc[i][c] = fmaf(v[j][c], f.x, acc[i][c]);
-            acc[i + 1][c] = fmaf(v[j][c], f.y, acc[i + 1][c]);
-            acc[i + 2][c] = fmaf(v[j][c], f.z, acc[i + 2][c]);
-            acc[i + 3][c] = fmaf(v[j][c], f.w, acc[i + 3][c]);
+          for (int i = 0; i < NE; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(xr + i);
+            xe[i] = f.x;
+            xe[i + 1] = f.y;
+            xe[i + 2] = f.z;
+            xe[i + 3] = f.w;
           }
         }
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) acc[i][c] = fmaf(v[j][c], xe[i], acc[i][c]);
       }
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kGenEntries; ++i)
+  for (int i = 0; i < NE; ++i)
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
       float v = acc[i][c];
@@ -969,6 +972,15 @@ __device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& 
       if (sub == 0) sh.part[warp][i][lane * VEC + c] = v;
     }
   __syncthreads();
+}
+
+template <typename T, int VEC, typename In>
+__device__ __forceinline__ void gen_multiply(const GenArgs<T>& g, const Tables& tb, GenShared& sh, const Pass& p, int kg,
+                                             int bi, const T* w, long long ldw, bool on, int wi, int warps, int part,
+                                             int parts, In in) {
+  if (p.n <= 2) gen_multiply_entries<T, VEC, 2>(g, tb, sh, p, kg, bi, w, ldw, on, wi, warps, part, parts, in);
+  else if (p.n <= 4) gen_multiply_entries<T, VEC, 4>(g, tb, sh, p, kg, bi, w, ldw, on, wi, warps, part, parts, in);
+  else gen_multiply_entries<T, VEC, kGenEntries>(g, tb, sh, p, kg, bi, w, ldw, on, wi, warps, part, parts, in);
 }
 
 template <typename T, int VEC>
@@ -1111,14 +1123,16 @@ static aal_status run_up(ExpertArgs a, size_t tables, cudaStream_t s) {
   a.ntile = a.q * a.tiles;
   a.by_tiles = tc::make_fastdiv((uint32_t)a.tiles);
   a.by_ntile = tc::make_fastdiv((uint32_t)a.ntile);
-  // clusters for the pieces left over, while every warp of one keeps two steps
+  const long long pieces = (long long)a.ntile * a.passes, room = 2LL * sms;
+  // clusters while each piece has one to itself and every warp two steps (one
+  // token of 2 experts, 24 pieces: 20.5 us a step against 22.8 without; of 8,
+  // 96 pieces in turns: 36.1 against 33.2; clusters of two for one token of 8
+  // experts under Q_16, 128 pieces: 21.4 against 18.1)
   const int steps = (a.q < 2 ? 1 : 2) * (bi >> 4);
-  const int z = steps >= 32 ? 4 : 1;
+  const int z = 4 * pieces <= room && steps >= 32 ? 4 : 1;
   a.zsplit = z;
-  const int used = a.B * a.k < a.E ? a.B * a.k : a.E;
-  const long long pieces = (long long)a.ntile * used * z, room = 2LL * sms / z * z;
   return timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch_pdl<k_moe_up<NT, S>>(dim3((unsigned)(pieces < room ? pieces : room)), kThreads, up_bytes<NT, S>() + tables,
+    return launch_pdl<k_moe_up<NT, S>>(dim3((unsigned)(pieces * z < room ? pieces * z : room)), kThreads, up_bytes<NT, S>() + tables,
                   z > 1 ? z : 0, s, a);
   });
 }
