@@ -8,8 +8,11 @@ the pre-activation and gradient workspaces it passes to the library.
 
 ``layer_norm(X, gamma, beta)`` is the norm of X's rows, and with ``residual``
 the pair (norm of X + residual, the sum).  ``swiglu_block`` is the pre-norm
-feed-forward sublayer X + swiglu(layer_norm(X)).  All arithmetic runs in the
-CUDA library.
+feed-forward sublayer X + swiglu(layer_norm(X)).  All arithmetic but that
+sublayer's residual add runs in the CUDA library.
+
+To capture a backward into a CUDA graph, first let go of every eager graph that
+reaches the same leaves (its losses and outputs), as torch requires.
 """
 from __future__ import annotations
 
