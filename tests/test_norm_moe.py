@@ -569,6 +569,12 @@ MOE = [
     (75, 40, 31, 64, 32, "Q", 2, "bf16", 0),       # chains of 33 entries
     (128, 2048, 8, 32, 16, "Q", 1, "bf16", 0),     # the largest tables
     (128, 2048, 8, 32, 17, "Q", 1, "bf16", 0),
+    # pieces of few steps, several a CTA
+    (64, 128, 8, 256, 256, "Q", 16, "bf16", 8),
+    (32, 128, 32, 256, 256, "Q", 16, "bf16", 0),
+    (61, 128, 8, 512, 768, "Q", 8, "bf16", 0),
+    (64, 128, 8, 128, 656, "Q", 1, "bf16", 0),
+    (33, 100, 8, 64, 1088, "Q2xQ2", 4, "bf16", 16),
     (3, 700, 9, 48, 80, "Q", 1, "f32", 0),         # experts beyond the counted ranking
     (9, 6, 6, 300, 150, "Q", 150, "bf16", 0),      # groups of two and of one
     (5, 12, 3, 202, 62, "Q", 2, "f32", 2),         # vectors off by two
