@@ -1008,19 +1008,22 @@ static bool rows_aligned(const aal_mat& m) {
   return !m.ptr || (((uintptr_t)m.ptr % 16) == 0 && (m.rows <= 1 || (m.ld * es) % 16 == 0));
 }
 
-// Raises kernel K's limit of dynamic shared memory to ``bytes`` on the current
-// device, once (the driver call costs as much as a short kernel).
+// Raises kernel K's limit of dynamic shared memory on the current device to all
+// that its static arrays leave, once (the driver call costs as much as a short
+// kernel).  Without it 48 KB hold, of static and dynamic memory together: what
+// a launch may ask for then depends on the kernel's static arrays, so every
+// kernel with dynamic memory is raised, whatever its first launch needs.
 template <auto K>
 static cudaError_t allow_shared(size_t bytes) {
   constexpr int kDevices = 64;
   static std::atomic<size_t> allowed[kDevices];
-  if (bytes <= 32 * 1024) return cudaSuccess;  // (the static arrays count too)
+  if (bytes == 0) return cudaSuccess;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::atomic<size_t>* a = dev >= 0 && dev < kDevices ? &allowed[dev] : nullptr;
   if (a && a->load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
-  // two threads may come here together: the limit only ever grows
+  // two threads may come here together: both raise the limit to the same value
   int most = 0;
   e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   cudaFuncAttributes f;
