@@ -19,7 +19,7 @@
 // Measured, microseconds a call in a graph, against the bytes at the copy rate
 // of 6.53 TB/s:  forward 12288 x 768 bf16 with residual 16.0 (11.6), 2048 x
 // 4096 fp32 17.0 (10.3), 4099 x 1003 bf16 10.1 (2.5);  backward 32768 x 5120
-// bf16 with dR 209 (205), 12288 x 768 22.5 (11.6), 2047 x 1001 fp32 17-18
+// bf16 with dR 207 (205), 12288 x 768 22.5 (11.6), 2047 x 1001 fp32 17-18
 // (3.8), 96 x 2048 7.4.  Large calls are bound by HBM; those of a few rows a
 // CTA by the ring's start, the reductions of the rows and, backward, the second
 // launch.
@@ -327,6 +327,27 @@ __device__ __forceinline__ void row_get(uint32_t row, int i, int tpr, int left, 
     for (int j = 0; j < Vec<T>::pairs; ++j) v[j] = pair(e[2 * j], e[2 * j + 1]);
   }
 }
+// A thread's vector i of a row less the row's mean.  bf16 elements are widened by
+// the addition itself, one mixed-precision instruction an element (32768 x 5120
+// backward 207 us; with a pair addition after the widening 217.5).
+template <typename T, bool ELEM, int TPR>
+__device__ __forceinline__ void row_get_less(uint32_t row, int i, int tpr, int left, float mean,
+                                             f32x2 (&v)[Vec<T>::pairs]) {
+  if constexpr (!ELEM && sizeof(T) == 2) {
+    const uint4 u = lds128(row + i * tpr * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 a, b;\n\tmov.b32 {lo, hi}, %1;\n\tadd.rn.f32.bf16 a, lo, %2;\n\t"
+          "add.rn.f32.bf16 b, hi, %2;\n\tmov.b64 %0, {a, b};\n\t}"
+          : "=l"(v[j])
+          : "r"(w[j]), "f"(-mean));
+  } else {
+    row_get<T, ELEM, TPR>(row, i, tpr, left, v);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::pairs; ++j) v[j] = add2(v[j], pair(-mean, -mean));
+  }
+}
 template <typename T, bool ELEM, int TPR>
 __device__ __forceinline__ void row_put(T* row, int i, int tpr, int left, const f32x2 (&v)[Vec<T>::pairs]) {
   constexpr int n = Vec<T>::n;
@@ -584,15 +605,18 @@ struct BwdArgs {
   uint32_t ring_bytes;
 };
 
-// dx = rstd (g - mean(g) - xh mean(g xh)) as g rstd + A + B x: the row's two
-// numbers are folded once instead of recomputing xh for every element.
+// dx = rstd (g - mean(g) - xh mean(g xh)) as g rstd + A + B (x - mu), the row's
+// two numbers folded once.  The mean is subtracted from x, where the difference
+// is rounded against itself: with -B mu folded into A instead, two large numbers
+// would cancel in rows far from zero (relative error of dx 5e-5 instead of 8e-8
+// at a mean of 1000 standard deviations).
 struct RowFold {
   float A, B;
 };
-__device__ __forceinline__ RowFold fold_row(float mu, float rs, float mg, float mgx) {
+__device__ __forceinline__ RowFold fold_row(float rs, float mg, float mgx) {
   RowFold f;
-  f.B = -rs * rs * mgx;
-  f.A = -rs * mg - f.B * mu;
+  f.A = -rs * mg;
+  f.B = -rs * (rs * mgx);
   return f;
 }
 
@@ -719,17 +743,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
     ring_wait(&bar[st], ph);
     if (ELEM) gr.sync();
     f32x2 sg = 0, sgx = 0;
-    const f32x2 nmu = pair(-mu, -mu), rs2 = pair(rs, rs);
+    const f32x2 rs2 = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i] || !on) continue;
       f32x2 xv[P], yv[P], w[P];
-      row_get<T, ELEM, TPR>(m, i, tpr, left, xv);
+      row_get_less<T, ELEM, TPR>(m, i, tpr, left, mu, xv);
       row_get<T, ELEM, TPR>(my, i, tpr, left, yv);  // zero past the row, and with it every product below
       if (gm) gamma(i, w);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const f32x2 xh = mul2(add2(xv[j], nmu), rs2);
+        const f32x2 xh = mul2(xv[j], rs2);
         const f32x2 g = gm ? mul2(yv[j], w[j]) : yv[j];
         sg = add2(sg, g);
         sgx = fma2(g, xh, sgx);
@@ -744,20 +768,20 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
       if (gr.lane == 0 && next < blocks && rb != gr.first) fill(next, before);
     }
     if (a.dx && on) {
-      const RowFold f = fold_row(mu, rs, s.x * inv_d, s.y * inv_d);
+      const RowFold f = fold_row(rs, s.x * inv_d, s.y * inv_d);
       const f32x2 A = pair(f.A, f.A), B = pair(f.B, f.B);
       T* o = (T*)a.dx + row * a.lddx + t * (ELEM ? 1 : VEC);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
         f32x2 xv[P], yv[P], w[P];
-        row_get<T, ELEM, TPR>(m, i, tpr, left, xv);
+        row_get_less<T, ELEM, TPR>(m, i, tpr, left, mu, xv);
         row_get<T, ELEM, TPR>(my, i, tpr, left, yv);
         if (gm) gamma(i, w);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           const f32x2 g = gm ? mul2(yv[j], w[j]) : yv[j];
-          xv[j] = fma2(g, rs2, fma2(xv[j], B, A));
+          xv[j] = fma2(g, rs2, fma2(xv[j], B, A));  // xv: x - mu
         }
         if (dr) {
           row_get<T, ELEM, TPR>(mr, i, tpr, left, w);

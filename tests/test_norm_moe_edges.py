@@ -1,15 +1,24 @@
-"""Edges of the layer norm and of the experts' step."""
+"""Edges of the layer norm and of the experts' step.
+
+Bounds are counted from the arithmetic: U = 2^-24 for a rounding to fp32, half
+a step of the output's type (relative 2^-8 for bf16, 2^-24 for fp32) for the
+last one."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
 
-from test_norm_moe import cuda  # noqa: F401 (a fixture)
+import oracle
+import associative_algebra_block_b200 as aal
+from test_norm_moe import HALF, TD, cuda, h64  # noqa: F401 (a fixture)
 
 gpu = pytest.mark.gpu
+U = 2.0 ** -24
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -73,3 +82,53 @@ def test_general_experts_launch_as_the_first_calls_of_a_process(cuda, band, capt
     script = FIRST_GENERAL_CALLS.format(root=ROOT, tests=os.path.join(ROOT, "tests"), shapes=shapes, captured=captured)
     done = subprocess.run([sys.executable, "-c", script], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+# ----------------------------------------------------- the backward far from zero
+# dx = rstd (g - mean(g) - xh mean(g xh)), every rounding counted:
+#   a sum over the row   E = (d / 1024 + 32) u of its terms' magnitudes (a thread's
+#                        elements, two trees), and 2 u for the division by d;
+#   xh                   2 u (x - mean is rounded against itself, then times rstd)
+#                        and as much again within a sum's terms, g u;
+#   the three terms      g rstd: 2 u;  rstd mean(g): 3 u;  (x - mean) rstd^2 mean(g xh): 6 u
+#                        (in whichever order the factors are taken);
+#   their two additions  u of what they add, the first of which counts twice above;
+#   then dR, and the output's own rounding.
+# Nothing is rounded against x or mean, so the bound does not grow with the offset.
+def _bwd_bound(x, mean, rstd, g, ref, d):
+    xh = np.abs((x - mean) * rstd)
+    e = (d / 1024 + 32) * U
+    mg, mgx = np.abs(g).mean(1, keepdims=True), (np.abs(g) * xh).mean(1, keepdims=True)
+    return rstd * ((4 * U) * np.abs(g) + (e + 8 * U) * mg + xh * (e + 14 * U) * mgx) + 2 * U * np.abs(ref)
+
+
+@gpu
+@pytest.mark.parametrize("offset", [0.0, 10.0, 100.0, 1000.0, 10000.0])
+@pytest.mark.parametrize("m,d,dtype,affine", [
+    (300, 40, "f32", "f32"),      # several rows a warp
+    (70, 500, "f32", "f32"), (33, 333, "f32", None),
+    (64, 1024, "f32", "f32"), (37, 1501, "f32", "f32"), (5, 8192, "f32", "f32"), (3, 5001, "f32", None),
+    (3, 9000, "f32", "f32"),      # walked twice
+    (65, 768, "bf16", "f32"), (33, 2048, "bf16", "bf16")])
+def test_layer_norm_bwd_of_rows_with_an_offset(cuda, m, d, dtype, affine, offset):
+    gen = torch.Generator().manual_seed(m + d)
+    X = (torch.randn(m, d, generator=gen) + offset).to(TD[dtype])
+    x = X.double().numpy()
+    mean, rstd = (torch.from_numpy(v).float() for v in oracle.layer_norm(x)[1:])
+    mu, rs = mean.double().numpy()[:, None], rstd.double().numpy()[:, None]
+    # a gradient that goes with the row: every term of dx counts
+    dY = (torch.randn(m, d, generator=gen) + torch.from_numpy((x - mu) * rs)).to(TD[dtype])
+    gamma = (torch.randn(d, generator=gen) * 0.1 + 1).to(TD[affine]) if affine else None
+    res = m % 2 == 1
+    dR = torch.randn(m, d, generator=gen).to(TD[dtype]) if res else None
+    dX = torch.full((m, d), float("nan"), dtype=TD[dtype], device="cuda")
+    dev = [None if t is None else t.cuda() for t in (X, gamma, mean, rstd, dY, dR)]
+    aal.aal_layer_norm_bwd(*dev[:5], dX=dX, dR=dev[5])
+    g64 = None if gamma is None else gamma.double().numpy()
+    dy = dY.double().numpy()
+    ref, _, _ = oracle.layer_norm_bwd(x, g64, mu[:, 0], rs[:, 0], dy)
+    err = _bwd_bound(x, mu, rs, dy if gamma is None else dy * g64, ref, d)
+    if res:
+        ref = ref + dR.double().numpy()
+        err = err + U * np.abs(ref)
+    assert (np.abs(h64(dX) - ref) <= HALF[dtype] * np.abs(ref) + 1.01 * err).all()
