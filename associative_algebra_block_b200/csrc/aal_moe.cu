@@ -1191,19 +1191,24 @@ static aal_status run_general(const ExpertArgs& e, const aal_mat& x, const aal_m
   a.by_k = tc::make_fastdiv((uint32_t)a.k);
   const size_t tables = Tables::bytes(a.passes, a.E, a.B, a.k);
   const int sms = device_sms();
+  auto divisor = [](int n) { return tc::make_fastdiv((uint32_t)(n > 0 ? n : 1)); };  // (of an empty width: not used)
   auto tiles = [&](int bo, int bi) {
     a.tiles = (bo + kGenTile - 1) / kGenTile;
     a.ntile = a.q * a.tiles;
-    a.by_tiles = tc::make_fastdiv((uint32_t)a.tiles);
-    a.by_ntile = tc::make_fastdiv((uint32_t)a.ntile);
-    g.by_bi = tc::make_fastdiv((uint32_t)bi);
+    a.by_tiles = divisor(a.tiles);
+    a.by_ntile = divisor(a.ntile);
+    g.by_bi = divisor(bi);
   };
   tiles(a.F / a.q, a.D / a.q);
   const long long pieces = (long long)a.ntile * a.passes, room = 2LL * sms;
+  // F = 0: one CTA without a piece, so that the down kernel still starts after
+  // the router's end
+  const unsigned grid = pieces < 1 ? 1 : (unsigned)(pieces < room ? pieces : room);
   aal_status st = timed(AAL_KERNEL_MOE_UP, s, [&] {
-    return launch_pdl<k_moe_up_general<T, VEC>>(dim3((unsigned)(pieces < room ? pieces : room)), kThreads, tables, 0, s, g);
+    return launch_pdl<k_moe_up_general<T, VEC>>(dim3(grid), kThreads, tables, 0, s, g);
   });
   if (st != AAL_OK) return st;
+  if (a.D == 0) return AAL_OK;  // y has no elements
   tiles(a.D / a.q, a.F / a.q);
   return timed(AAL_KERNEL_MOE_DOWN, s, [&] {
     return launch_pdl<k_moe_down_general<T, VEC>>(dim3((unsigned)(a.ntile * kDownCtas)), kThreads,
@@ -1238,11 +1243,12 @@ extern "C" aal_status aal_moe_decode(int32_t law, int32_t q, const int64_t* posi
   if (((uintptr_t)positions % 8) || ((uintptr_t)ids % 4) || ((uintptr_t)weights % 4)) return AAL_ERR_INVALID_ARG;
   if (B > 0 && (!positions || !ids || !weights)) return AAL_ERR_INVALID_ARG;
   note_path(0);
-  if (B == 0 || D == 0 || F == 0) return AAL_OK;
+  if (B == 0) return AAL_OK;
   cudaStream_t s = (cudaStream_t)stream;
-  const bool fast = t_policy != AAL_PATH_GENERAL && dt == AAL_BF16 && q <= moe::kMaxQ && (D / q) % 16 == 0 &&
-                    (F / q) % 16 == 0 && moe::vec16(x) && moe::vec16(Wg) && moe::vec16(Wu) && moe::vec16(Wd) &&
-                    moe::vec16(h);
+  // (empty widths leave no tile to multiply: the general path takes the empty sums)
+  const bool fast = t_policy != AAL_PATH_GENERAL && dt == AAL_BF16 && q <= moe::kMaxQ && D > 0 && F > 0 &&
+                    (D / q) % 16 == 0 && (F / q) % 16 == 0 && moe::vec16(x) && moe::vec16(Wg) && moe::vec16(Wu) &&
+                    moe::vec16(Wd) && moe::vec16(h);
   if (!fast && t_policy == AAL_PATH_TENSOR) return AAL_ERR_UNSUPPORTED;
   const size_t es = dt == AAL_F32 ? 4 : 2;
   const bool wvec = moe::vec16(Wg) && moe::vec16(Wu) && moe::vec16(Wd) && (D / q) % 4 == 0 && (F / q) % 4 == 0;

@@ -313,6 +313,8 @@ AAL_API int64_t aal_layer_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  *   positions: device int64 [B]; x [B, D]; Wr [D, E]; the experts stacked by
  *   rows: Wg, Wu [E D, F] (expert e is rows e D .. e D + D - 1), Wd [E F, D];
  *   R [B, D] (ptr == NULL: no residual).
+ *   D or F may be 0: sums over nothing are 0 (F = 0: y is the residual or 0;
+ *   D = 0: all logits tie).
  *   ids: device int32 [B, k], weights: device fp32 [B, k]: the choices in
  *   order of falling logit, overwritten.  h [B k, F]: caller's workspace,
  *   overwritten with the activations of the choices.  y [B, D]: overwritten;

@@ -15,7 +15,7 @@ import torch
 
 import oracle
 import associative_algebra_block_b200 as aal
-from test_norm_moe import HALF, TD, cuda, h64  # noqa: F401 (a fixture)
+from test_norm_moe import HALF, TD, Moe, cuda, h64  # noqa: F401 (a fixture)
 
 gpu = pytest.mark.gpu
 U = 2.0 ** -24
@@ -132,3 +132,51 @@ def test_layer_norm_bwd_of_rows_with_an_offset(cuda, m, d, dtype, affine, offset
         ref = ref + dR.double().numpy()
         err = err + U * np.abs(ref)
     assert (np.abs(h64(dX) - ref) <= HALF[dtype] * np.abs(ref) + 1.01 * err).all()
+
+
+# ------------------------------------------------------------------ empty widths
+def _narrowed(m, D, F):
+    """The step with D or F set to 0."""
+    m.x, m.Wr, m.y = m.x[:, :D], m.Wr[:D], m.y[:, :D]
+    m.Wg, m.Wu, m.Wd, m.h = m.Wg[:m.E * D, :F], m.Wu[:m.E * D, :F], m.Wd[:m.E * F, :D], m.h[:, :F]
+    m.D, m.F = D, F
+    return m
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("B", [1, 5, 20, 150])
+def test_moe_of_width_zero_is_the_residual_and_the_choices(cuda, B, renorm, dtype):
+    """F = 0: every expert's product is an empty sum, so y is R (or zero), and
+    the router's choices do not depend on F."""
+    for residual in (True, False):
+        m = _narrowed(Moe(B, 12, 3, 64, 32, "Q", 2, dtype, seed=B, residual=residual), 64, 0)
+        if B > 1:
+            m.pos[1] = -1  # skipped: its row stays
+        m.y.fill_(3.5)
+        m.run(renormalize=renorm)
+        rows = np.array([b for b in range(B) if b != 1])
+        ids, w = oracle.route(h64(m.x)[rows], h64(m.Wr), 3, renorm)
+        assert np.array_equal(m.ids.cpu().numpy()[rows], ids)
+        assert (np.abs(h64(m.w)[rows] - w) <= 64 * U * w + 1e-38).all()
+        want = m.R if residual else torch.zeros_like(m.y)
+        assert torch.equal(m.y[rows], want[rows])
+        if B > 1:
+            assert (m.y[1] == 3.5).all() and (m.ids[1] == -1).all() and (m.w[1] == 0).all()
+        assert aal.aal_get_device_status() == (aal.AAL_ERR_DEVICE_BOUNDS if B > 1 else aal.AAL_OK)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_moe_of_inputs_of_width_zero(cuda, dtype):
+    """D = 0: every logit is an empty sum, so all tie and the lower indices win;
+    h is silu(0) * 0."""
+    m = _narrowed(Moe(21, 6, 2, 64, 32, "Q", 2, dtype, residual=False), 0, 32)
+    for renorm, weight in ((True, 1 / 2), (False, 1 / 6)):
+        m.ids.fill_(-7)
+        m.h.fill_(3.5)
+        m.run(renormalize=renorm)
+        assert m.ids.tolist() == [[0, 1]] * 21 and (m.h == 0).all()
+        assert (np.abs(h64(m.w) - weight) <= 64 * U * weight).all()
+    assert aal.aal_get_device_status() == aal.AAL_OK
