@@ -977,7 +977,7 @@ static Plan plan(long long d, int es, bool aligned, int arrays, int pes) {
   Plan p = {};
   const int vec = 16 / es;
   p.elem = !(aligned && (d * es) % 16 == 0);
-  p.wide = d > (p.elem ? 512 * 16 : 1024 * 16);
+  p.wide = d == 0 || d > (p.elem ? 512 * 16 : 1024 * 16);  // (no element: only the statistics, 0 / 0)
   p.block = !p.wide && d > (p.elem ? 32 * 16 : 32 * 4 * vec);
   p.nv = 1;
   p.lpr = 32;
@@ -1193,7 +1193,7 @@ aal_status aal_layer_norm_fwd(aal_mat X, aal_mat R, aal_mat gamma, aal_mat beta,
   if (((uintptr_t)mean | (uintptr_t)rstd) % 4) return AAL_ERR_INVALID_ARG;
   if (M > 0 && d > 0 && S.ptr && S.ptr == Y.ptr) return AAL_ERR_INVALID_ARG;
   note_path(0);
-  if (M == 0 || d == 0) return AAL_OK;
+  if (M == 0 || (d == 0 && !mean && !rstd)) return AAL_OK;
   const int pdt = gamma.ptr ? gamma.dtype : beta.ptr ? beta.dtype : dt;
   const bool al = norm::rows_aligned(X) && norm::rows_aligned(R) && norm::rows_aligned(S) && norm::rows_aligned(Y) &&
                   norm::rows_aligned(gamma) && norm::rows_aligned(beta);

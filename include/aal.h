@@ -265,7 +265,8 @@ AAL_API aal_status aal_square_product(int32_t law, int32_t q, aal_mat X, aal_mat
  *   unrounded sum.
  *   gamma, beta [1, d] in the call's dtype or both in AAL_F32; ptr == NULL
  *   stands for ones and zeros.
- *   mean, rstd: device fp32 arrays of M entries, or NULL.
+ *   mean, rstd: device fp32 arrays of M entries, or NULL (d = 0: NaN, the
+ *   mean of no element).
  *   S and Y may be X or R themselves (same pointer and ld), not each other;
  *   other overlaps are not allowed.  eps >= 0 and finite.
  * Any M, d and ld.  Rows whose pointers and leading dimensions are multiples

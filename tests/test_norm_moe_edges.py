@@ -180,3 +180,16 @@ def test_moe_of_inputs_of_width_zero(cuda, dtype):
         assert m.ids.tolist() == [[0, 1]] * 21 and (m.h == 0).all()
         assert (np.abs(h64(m.w) - weight) <= 64 * U * weight).all()
     assert aal.aal_get_device_status() == aal.AAL_OK
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_of_rows_of_width_zero(cuda, dtype):
+    """d = 0: the statistics are those of no element, 0 / 0."""
+    X = torch.empty(700, 0, dtype=TD[dtype], device="cuda")
+    mean, rstd = torch.zeros(700, device="cuda"), torch.zeros(700, device="cuda")
+    aal.aal_layer_norm_fwd(X, None, None, X, R=X, S=X, mean=mean, rstd=rstd)
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+    aal.aal_layer_norm_fwd(X, None, None, X)
+    aal.aal_layer_norm_bwd(X, None, mean, rstd, X, dX=X)
+    torch.cuda.synchronize()
