@@ -31,9 +31,9 @@ static cudaError_t record_event(cudaEvent_t e, cudaStream_t s) {
 template <typename F>
 static aal_status timed(int kind, cudaStream_t s, F launch) {
   cudaEvent_t b = t_ev_before[kind], a = t_ev_after[kind];
-  if (b && record_event(b, s) != cudaSuccess) return AAL_ERR_CUDA;
-  aal_status st = launch();
-  if (a && st == AAL_OK && record_event(a, s) != cudaSuccess) return AAL_ERR_CUDA;
+  aal_status st = b ? cuda_status(record_event(b, s)) : AAL_OK;
+  if (st == AAL_OK) st = launch();
+  if (a && st == AAL_OK) st = cuda_status(record_event(a, s));
   if (st == AAL_OK) { t_ev_before[kind] = nullptr; t_ev_after[kind] = nullptr; }
   return st;
 }

@@ -1041,7 +1041,7 @@ aal_status decode_gate_up(int law, int q, const int64_t* positions, const aal_ma
     else if (nb <= 64) e = launch_mma<4, true>(cl, law, q, positions + b0, nb, xs, Wg, &Wu, hs, bi, bo, dout, s);
     else e = launch_mma<8, true>(cl, law, q, positions + b0, nb, xs, Wg, &Wu, hs, bi, bo, dout, s);
     note_launch();
-    if (e != cudaSuccess) return AAL_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_status(e);
   }
   return AAL_OK;
 }

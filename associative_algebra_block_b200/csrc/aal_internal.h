@@ -165,6 +165,13 @@ aal_status seg_swiglu_fwd(int law, int q, const RowTypes& rt, const aal_mat& X, 
                           const aal_mat& Wu, const aal_mat& Wd, const aal_mat& H, const aal_mat& Y, void* ws,
                           uint64_t ws_bytes, cudaStream_t s);
 
-inline aal_status cuda_status(cudaError_t e) { return e == cudaSuccess ? AAL_OK : AAL_ERR_CUDA; }
+// The status of a runtime call.  The runtime keeps a failed call's error for
+// cudaGetLastError, which is how launches are checked: it is taken here, so that
+// the next launch is not blamed for it.
+inline aal_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return AAL_OK;
+  (void)cudaGetLastError();
+  return AAL_ERR_CUDA;
+}
 
 }  // namespace aal

@@ -1065,7 +1065,7 @@ static cudaError_t allow_shared(size_t bytes) {
 // cluster size at launch.
 template <auto K, typename... A>
 static aal_status launch_pdl(dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args) {
-  if (allow_shared<K>(smem) != cudaSuccess) return AAL_ERR_CUDA;
+  if (const aal_status st = cuda_status(allow_shared<K>(smem)); st != AAL_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);

@@ -193,3 +193,44 @@ def test_layer_norm_of_rows_of_width_zero(cuda, dtype):
     aal.aal_layer_norm_fwd(X, None, None, X)
     aal.aal_layer_norm_bwd(X, None, mean, rstd, X, dX=X)
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------- what a refused launch leaves
+# A stream refuses launches once something not allowed in a capture (waiting for
+# it) has ended the capture it is in.  The call says so, and the calls after it,
+# some of which check their launches by the runtime's last error, are not blamed.
+REFUSED_LAUNCH = """
+import ctypes
+import torch
+import associative_algebra_block_b200 as aal
+
+cu = ctypes.CDLL("libcuda.so.1")
+X, Y = torch.randn(4, 64, device="cuda"), torch.empty(4, 64, device="cuda")
+W, P = torch.randn(64, 32, device="cuda"), torch.empty(4, 32, device="cuda")
+pos = torch.arange(4, device="cuda")
+s = torch.cuda.Stream()
+aal.aal_layer_norm_fwd(X, None, None, Y, stream=s)
+aal.aal_decode_matvec("Q", 2, pos, X, W, P)
+torch.cuda.synchronize()
+want = P.clone()
+P.zero_()
+torch.cuda.synchronize()
+stream, graph = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p()
+assert cu.cuStreamBeginCapture_v2(stream, 2) == 0
+assert cu.cuStreamSynchronize(stream) != 0
+try:
+    aal.aal_layer_norm_fwd(X, None, None, Y, stream=s)
+    raise SystemExit("the launch was not refused")
+except aal.AalError as e:
+    assert e.status == aal.AAL_ERR_CUDA
+assert cu.cuStreamEndCapture(stream, ctypes.byref(graph)) != 0
+aal.aal_decode_matvec("Q", 2, pos, X, W, P)
+torch.cuda.synchronize()
+assert torch.equal(P, want)
+"""
+
+
+@gpu
+def test_a_refused_launch_leaves_no_error_behind(cuda):
+    done = subprocess.run([sys.executable, "-c", REFUSED_LAUNCH], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
