@@ -215,6 +215,18 @@ static int ready(Py_ssize_t n, Py_ssize_t want, const void* fn) {
   return 0;
 }
 
+/* Returns the library call's status.  Other threads run meanwhile: a launch may
+ * wait for room in the stream's queue, or for a kernel to be loaded.  (The
+ * tensors stay alive: the caller's arguments hold them.) */
+#define CALL(call)                  \
+  do {                              \
+    aal_status status;              \
+    Py_BEGIN_ALLOW_THREADS          \
+    status = call;                  \
+    Py_END_ALLOW_THREADS            \
+    return PyLong_FromLong(status); \
+  } while (0)
+
 /* (X, gamma, beta, Y, eps, R, S, mean, rstd, stream) */
 static PyObject* norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   call_ctx c = {kNone};
@@ -231,7 +243,7 @@ static PyObject* norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return NULL;
   const double eps = PyFloat_AsDouble(a[4]);
   if (eps == -1.0 && PyErr_Occurred()) return NULL;
-  return PyLong_FromLong(f_norm_fwd(X, R, g, b, (float)eps, S, Y, (float*)mean, (float*)rstd, stream));
+  CALL(f_norm_fwd(X, R, g, b, (float)eps, S, Y, (float*)mean, (float*)rstd, stream));
 }
 
 /* (X, gamma, mean, rstd, dY, dX, dgamma, dbeta, dR, accumulate, stream) */
@@ -249,8 +261,7 @@ static PyObject* norm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (X.cols && (not_empty(a[1], &g, "gamma") || not_empty(a[6], &dg, "dgamma") || not_empty(a[7], &db, "dbeta")))
     return NULL;
   if (X.ptr && (not_empty(a[8], &dR, "dR") || not_empty(a[5], &dX, "dX"))) return NULL;
-  return PyLong_FromLong(
-      f_norm_bwd(X, g, (const float*)mean, (const float*)rstd, dY, dR, dX, dg, db, acc, stream));
+  CALL(f_norm_bwd(X, g, (const float*)mean, (const float*)rstd, dY, dR, dX, dg, db, acc, stream));
 }
 
 /* (law, q, positions, x, Wr, Wg, Wu, Wd, ids, weights, h, y, R, renormalize, stream) */
@@ -280,8 +291,8 @@ static PyObject* moe(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       get_array(&c, a[9], d_f32, rows * k, "weights", &wt) || get_stream(&c, a[14], &stream))
     return NULL;
   if (x.ptr && not_empty(a[12], &r, "R")) return NULL;
-  return PyLong_FromLong(f_moe((int32_t)law, (int32_t)q, (const int64_t*)pos, x, wr, wg, wu, wd, r, (int32_t)k, renorm,
-                               (int32_t*)ids, (float*)wt, h, y, stream));
+  CALL(f_moe((int32_t)law, (int32_t)q, (const int64_t*)pos, x, wr, wg, wu, wd, r, (int32_t)k, renorm, (int32_t*)ids,
+             (float*)wt, h, y, stream));
 }
 
 /* (addresses of the three calls; torch.bfloat16, float32, int32, int64; the

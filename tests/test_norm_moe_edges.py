@@ -8,6 +8,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -15,7 +17,7 @@ import torch
 
 import oracle
 import associative_algebra_block_b200 as aal
-from test_norm_moe import HALF, TD, Moe, cuda, h64  # noqa: F401 (a fixture)
+from test_norm_moe import HALF, TD, Moe, cuda, h64, lib  # noqa: F401 (fixtures)
 
 gpu = pytest.mark.gpu
 U = 2.0 ** -24
@@ -234,3 +236,58 @@ assert torch.equal(P, want)
 def test_a_refused_launch_leaves_no_error_behind(cuda):
     done = subprocess.run([sys.executable, "-c", REFUSED_LAUNCH], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+# ------------------------------------------------------------------- the binding
+SLOW_CALL = r"""
+#include <unistd.h>
+#include "aal.h"
+__attribute__((visibility("default"))) aal_status slow_norm_fwd(aal_mat X, aal_mat R, aal_mat g, aal_mat b, float eps,
+    aal_mat S, aal_mat Y, float* m, float* r, void* s) { usleep(400000); return AAL_OK; }
+__attribute__((visibility("default"))) aal_status slow_norm_bwd(aal_mat X, aal_mat g, const float* m, const float* r,
+    aal_mat dY, aal_mat dR, aal_mat dX, aal_mat dg, aal_mat db, int32_t a, void* s) { usleep(400000); return AAL_OK; }
+__attribute__((visibility("default"))) aal_status slow_moe(int32_t law, int32_t q, const int64_t* p, aal_mat x, aal_mat wr,
+    aal_mat wg, aal_mat wu, aal_mat wd, aal_mat R, int32_t k, int32_t n, int32_t* i, float* w, aal_mat h, aal_mat y,
+    void* s) { usleep(400000); return AAL_OK; }
+"""
+
+
+def test_other_threads_run_while_the_library_is_called(lib, tmp_path, monkeypatch):
+    """The marshaller lets go of the interpreter for the call: a full launch
+    queue, or a stream that waits for another thread, must not stop that thread."""
+    import ctypes
+    src, so = tmp_path / "slow.c", tmp_path / "slow.so"
+    src.write_text(SLOW_CALL)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"), "-o", str(so), str(src)], check=True)
+    slow = ctypes.CDLL(str(so))
+    f = aal._fast()
+    addr = [ctypes.cast(getattr(slow, n), ctypes.c_void_p).value for n in ("slow_norm_fwd", "slow_norm_bwd", "slow_moe")]
+    rest = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.cuda.current_device, lambda dev: 0)
+    e, z = torch.empty(0, 8), torch.empty(0)
+    calls = [lambda: aal.aal_layer_norm_fwd(e, None, None, e),
+             lambda: aal.aal_layer_norm_bwd(e, None, z, z, e),
+             lambda: aal.aal_moe_decode("Q", 1, torch.empty(0, dtype=torch.int64), e, e, e, e, e,
+                                        torch.empty(0, 1, dtype=torch.int32), torch.empty(0, 1), e, e)]
+    f.setup(*addr, *rest)
+    try:
+        for call in calls:
+            ticks, stop = [], threading.Event()
+
+            def tick():
+                while not stop.is_set():
+                    ticks.append(time.monotonic())
+                    time.sleep(0.01)
+
+            t = threading.Thread(target=tick)
+            t.start()
+            t0 = time.monotonic()
+            call()
+            t1 = time.monotonic()
+            stop.set()
+            t.join()
+            assert t1 - t0 >= 0.3
+            # held, the thread would not tick between the call's first and last 0.1 s
+            assert any(t0 + 0.1 < v < t1 - 0.1 for v in ticks)
+    finally:
+        monkeypatch.setattr(aal, "_marshal", None)
+        aal._fast()
