@@ -7,7 +7,7 @@ only checks that tensors are 2-D, row-major and on the GPU, and raises
 ``AalError`` for a non-OK status.  The library is loaded on first use and a
 missing ``libaal.so`` is an error (build it with ``__graft_entry__.build()``
 or ``python -m associative_algebra_block_b200.build``).  The norm and expert
-calls go through a compiled marshaller (``_fastcall.so``, built with it).
+calls go through a compiled marshaller (``_fastcall``, built with it).
 """
 from __future__ import annotations
 

@@ -1,5 +1,5 @@
 """Builds libaal.so in-tree with nvcc for sm_100a, and the binding's small
-argument marshaller (_fastcall.so) with the C compiler.
+argument marshaller (_fastcall, a CPython extension) with the C compiler.
 
 Usage: ``python -m associative_algebra_block_b200.build`` (or
 ``__graft_entry__.build()``).  The library is one translation unit
@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libaal.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")
+# named for the interpreter whose headers it is built with
+FASTCALL = os.path.join(PKG, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -72,6 +73,9 @@ def build_fastcall() -> str:
                     sysconfig.get_paths()["include"], "-I", INCLUDE, "-o", tmp, os.path.join(SRC, "fastcall.c")],
                    check=True)
     os.replace(tmp, FASTCALL)
+    untagged = os.path.join(PKG, "_fastcall.so")  # an older build's: any interpreter would import it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     return FASTCALL
 
 

@@ -291,3 +291,14 @@ def test_other_threads_run_while_the_library_is_called(lib, tmp_path, monkeypatc
     finally:
         monkeypatch.setattr(aal, "_marshal", None)
         aal._fast()
+
+
+def test_the_marshaller_is_built_for_this_interpreter(lib):
+    """A file built with another interpreter's headers has another name and is
+    neither imported nor taken for built."""
+    import sysconfig
+    from associative_algebra_block_b200 import build
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert os.path.basename(build.FASTCALL) == "_fastcall" + suffix
+    assert os.path.samefile(aal._fast().__file__, build.FASTCALL)
+    assert not os.path.exists(os.path.join(build.PKG, "_fastcall.so"))
