@@ -502,8 +502,11 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
       }
     }
     const float mu = gr.sum(sum2(sum), buf, turn) * inv_d;
-    // A warp has its rows in registers; a CTA's threads are all done with the
-    // row before this one.
+    // A warp has its rows in registers, all its lanes' past the barrier; a CTA's
+    // threads are all done with the row before this one (the sum's barrier).
+    // The sum over a row's lanes alone would not order the other rows' reads
+    // before the copy that refills their stage.
+    if (!BLOCK) __syncwarp();
     const long long next = rb + (BLOCK ? S - 1 : S) * gr.step;
     if (gr.lane == 0 && next < blocks && (!BLOCK || rb != gr.first)) fill(next, BLOCK ? before : st);
     before = st;

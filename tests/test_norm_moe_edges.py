@@ -197,6 +197,34 @@ def test_layer_norm_of_rows_of_width_zero(cuda, dtype):
     torch.cuda.synchronize()
 
 
+# ------------------------------------------------ several rows a warp, many turns
+@gpu
+@pytest.mark.parametrize("m,d,dtype", [(60001, 8, "bf16"), (40003, 24, "f32"), (30007, 104, "bf16"), (9001, 768, "bf16")])
+def test_layer_norm_of_narrow_rows_repeats_itself(cuda, m, d, dtype):
+    """A warp refills a stage of its ring once all its rows have left it: the
+    same call again, in place and beside another one, gives the same bits."""
+    gen = torch.Generator().manual_seed(d)
+    X, R = (torch.randn(m, d, generator=gen).to(TD[dtype]).cuda() for _ in range(2))
+    Y, S = torch.empty_like(X), torch.empty_like(X)
+    aal.aal_layer_norm_fwd(X, None, None, Y, R=R, S=S)
+    ref, mu, rs = oracle.layer_norm(h64(X) + h64(R))
+    # sums of at most 32 elements a lane and five steps of a tree: (37 + 3) u for
+    # the mean against the row's largest element, twice and three times that for
+    # the variance's part and the product's
+    big = np.abs(h64(X) + h64(R)).max(1)[:, None] * rs[:, None]
+    assert (np.abs(h64(Y) - ref) <= HALF[dtype] * np.abs(ref) + 200 * U * big).all()
+    other = torch.cuda.Stream()
+    A, B = torch.randn(4096, 4096, device="cuda"), torch.empty(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(8):
+        with torch.cuda.stream(other):
+            aal.aal_layer_norm_fwd(A, None, None, B)
+        Xi, Ri = X.clone(), R.clone()
+        aal.aal_layer_norm_fwd(Xi, None, None, Ri, R=Ri, S=Xi)
+        assert torch.equal(Ri, Y) and torch.equal(Xi, S)
+    torch.cuda.synchronize()
+
+
 # --------------------------------------------------- what a refused launch leaves
 # A stream refuses launches once something not allowed in a capture (waiting for
 # it) has ended the capture it is in.  The call says so, and the calls after it,
