@@ -1114,7 +1114,9 @@ static aal_status with_shape(const Plan& p, F f) {
     }
   }
   if (p.block) {
-    if (BWD && p.threads <= 320) return f.template run<N, 0, false, false, 320, 2>();
+    if constexpr (BWD) {
+      if (p.threads <= 320) return f.template run<N, 0, false, false, 320, 2>();
+    }
     return p.threads <= 512 ? f.template run<N, 0, false, false, 512, BWD ? 1 : 2>()
                             : f.template run<N, 0, false, false, 1024, 1>();
   }
