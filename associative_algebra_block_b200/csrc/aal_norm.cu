@@ -7,9 +7,11 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh)) (+ dr)
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
-// Every byte of the matrices crosses HBM once, up to 16,384 columns (8,192
-// where rows start anywhere; wider rows are walked several times): a row comes
-// into shared memory while the ones before it are reduced, the variance is the
+// Every byte of the matrices crosses HBM once while two rows of every input fit
+// the ring: up to 16,384 columns, but 14,464 for fp32 rows with R and backward
+// with fp32 gamma, 8,264 for fp32 rows backward, and 8,192 where rows start
+// anywhere.  Wider rows are walked several times.  A row comes into shared memory
+// while the ones before it are reduced, the variance is the
 // mean of the squared distances from the mean (no cancellation), and the
 // backward keeps dgamma and dbeta of a thread's own columns in fp32 registers
 // over all the rows its CTA visits.  The CTAs' column sums go to the caller's

@@ -291,7 +291,10 @@ AAL_API aal_status aal_layer_norm_fwd(aal_mat X, aal_mat R, aal_mat gamma, aal_m
  * With the workspace of aal_set_workspace (aal_layer_norm_bwd_workspace_size
  * bytes) dX and the columns' sums come from one pass over X and dY: every CTA
  * leaves its sums there and a second launch adds them in a fixed order.
- * Without it dgamma and dbeta take a pass of their own, in a fixed order too.
+ * Without it dgamma and dbeta take a pass of their own, in a fixed order too,
+ * and so they do in any case for rows too wide to keep: above 16,384 bf16
+ * elements (14,464 with fp32 gamma) or 8,264 fp32 ones, and above 8,192 of
+ * either where rows move element by element.
  * M may be 0 (dgamma and dbeta are then zero, or unchanged when accumulating).
  */
 AAL_API aal_status aal_layer_norm_bwd(aal_mat X, aal_mat gamma, const float* mean, const float* rstd,
@@ -474,7 +477,8 @@ AAL_API int32_t aal_last_path(void);
  * entries the pair brackets all of the call's launches), AAL_KERNEL_NORM_FWD
  * (10), AAL_KERNEL_NORM_BWD (11, all launches of the call),
  * AAL_KERNEL_MOE_ROUTER, _UP and _DOWN (12, 13, 14: the launches of
- * aal_moe_decode, the first 128 entries' when there are more).
+ * aal_moe_decode, those of the first min(128, 1024 / top_k) entries when there
+ * are more).
  */
 enum { AAL_KERNEL_PROJECT = 1, AAL_KERNEL_GATE_UP = 2, AAL_KERNEL_BWD_DX = 3,
        AAL_KERNEL_BWD_DW = 4, AAL_KERNEL_SQUARE = 5, AAL_KERNEL_DECODE = 6,

@@ -136,6 +136,61 @@ def test_layer_norm_bwd_of_rows_with_an_offset(cuda, m, d, dtype, affine, offset
     assert (np.abs(h64(dX) - ref) <= HALF[dtype] * np.abs(ref) + 1.01 * err).all()
 
 
+# ------------------------------------------------ the widths that rings hold
+@gpu
+@pytest.mark.parametrize("d,dtype,affine,one_pass", [
+    (8264, "f32", "f32", True), (8268, "f32", "f32", False),
+    (14464, "bf16", "f32", True), (14472, "bf16", "f32", False),
+    (16384, "bf16", "bf16", True), (16392, "bf16", "bf16", False),
+    (8191, "f32", "f32", True), (8193, "f32", "f32", False),    # rows that start anywhere
+    (8191, "bf16", "f32", True), (8193, "bf16", "bf16", False)])
+def test_layer_norm_bwd_takes_one_pass_up_to_the_stated_widths(cuda, d, dtype, affine, one_pass):
+    """On both sides of each width: right, and the workspace used or not."""
+    m = 5
+    gen = torch.Generator().manual_seed(d)
+    X, dY = ((torch.randn(m, d, generator=gen) + s).to(TD[dtype]) for s in (3.0, 0.0))
+    gamma = (torch.randn(d, generator=gen) * 0.1 + 1).to(TD[affine])
+    x, dy, g64 = X.double().numpy(), dY.double().numpy(), gamma.double().numpy()
+    mean, rstd = (torch.from_numpy(v).float() for v in oracle.layer_norm(x)[1:])
+    mu, rs = mean.double().numpy()[:, None], rstd.double().numpy()[:, None]
+    ws = torch.full((max(256, aal.aal_layer_norm_bwd_workspace_size(m, d)),), 0x5a, dtype=torch.uint8, device="cuda")
+    dX = torch.empty(m, d, dtype=TD[dtype], device="cuda")
+    dg, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    dev = [t.cuda() for t in (X, gamma, mean, rstd, dY)]
+    aal.aal_set_workspace(ws)
+    try:
+        aal.aal_layer_norm_bwd(*dev, dX=dX, dgamma=dg, dbeta=db)
+    finally:
+        aal.aal_set_workspace(None)
+    assert bool((ws != 0x5a).any()) == one_pass
+    ref, rg, rb = oracle.layer_norm_bwd(x, g64, mu[:, 0], rs[:, 0], dy)
+    err = _bwd_bound(x, mu, rs, dy * g64, ref, d)
+    assert (np.abs(h64(dX) - ref) <= HALF[dtype] * np.abs(ref) + 1.01 * err).all()
+    # five rows: at most five additions and as many in the joining sums, xh 2 u
+    xh = np.abs((x - mu) * rs)
+    assert (np.abs(h64(dg) - rg) <= 13 * U * (np.abs(dy) * xh).sum(0) + U * np.abs(rg)).all()
+    assert (np.abs(h64(db) - rb) <= 11 * U * np.abs(dy).sum(0) + U * np.abs(rb)).all()
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,res", [(14464, "f32", True), (14468, "f32", True), (16384, "f32", False),
+                                         (16388, "f32", False), (16384, "bf16", True), (16392, "bf16", True),
+                                         (8191, "f32", True), (8193, "f32", True)])
+def test_layer_norm_fwd_on_both_sides_of_the_stated_widths(cuda, d, dtype, res):
+    m = 5
+    gen = torch.Generator().manual_seed(d)
+    X, R = (torch.randn(m, d, generator=gen).to(TD[dtype]).cuda() for _ in range(2))
+    Y, S = torch.empty_like(X), torch.empty_like(X)
+    aal.aal_layer_norm_fwd(X, None, None, Y, R=R if res else None, S=S if res else None)
+    s = h64(X) + (h64(R) if res else 0.0)
+    ref, mu, rs = oracle.layer_norm(s)
+    # a sum: (d / 1024 + 32) u; it enters by the mean, twice by the variance
+    big = np.abs(s).max(1)[:, None] * rs[:, None]
+    assert (np.abs(h64(Y) - ref) <= HALF[dtype] * np.abs(ref) + 4 * (d / 1024 + 32) * U * big).all()
+    if res:
+        assert (np.abs(h64(S) - s) <= (HALF[dtype] + U) * np.abs(s)).all()
+
+
 # ------------------------------------------------------------------ empty widths
 def _narrowed(m, D, F):
     """The step with D or F set to 0."""
@@ -223,6 +278,24 @@ def test_layer_norm_of_narrow_rows_repeats_itself(cuda, m, d, dtype):
         aal.aal_layer_norm_fwd(Xi, None, None, Ri, R=Ri, S=Xi)
         assert torch.equal(Ri, Y) and torch.equal(Xi, S)
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------------- long steps
+@gpu
+@pytest.mark.parametrize("B,E,k,D,F,law,q,dtype,pad", [
+    (300, 24, 3, 96, 64, "Q", 2, "bf16", 0),     # three chains of launches
+    (300, 8, 2, 40, 24, "Q", 2, "bf16", 0),      # the general path
+    (257, 16, 4, 64, 48, "Q", 2, "f32", 0)])
+def test_moe_of_many_entries(cuda, B, E, k, D, F, law, q, dtype, pad):
+    m = Moe(B, E, k, D, F, law, q, dtype, seed=B, pad=pad)
+    m.run()
+    assert aal.aal_get_device_status() == aal.AAL_OK
+    m.check()
+    y = m.y.clone()
+    for _ in range(5):
+        m.y.zero_()
+        m.run()
+        assert torch.equal(m.y, y)  # the same sums in the same order
 
 
 # --------------------------------------------------- what a refused launch leaves
