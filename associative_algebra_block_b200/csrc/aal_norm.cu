@@ -182,22 +182,26 @@ __device__ __forceinline__ void pdl_begin() {
 // elements TPR apart.
 constexpr int kMaxRing = 4;
 constexpr int kRowsPerCta = 8;  // groups of a CTA of warps
-constexpr unsigned long long kRingWaitNs = 2000000000ull;
+constexpr unsigned long long kRingWaitNs = 2000000000ull, kRingLostNs = 100000ull;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                : "memory");
 }
-// Bounded wait for a stage.  A copy that has not landed after two seconds
-// never will: the status word is set and the caller goes on with what is
-// there, so that every thread still reaches the kernel's barriers.
+// Bounded wait for a stage.  A copy that has not landed after two seconds never
+// will: the status word is set (in place of any other error) and the caller goes
+// on with what is there, so that every thread still reaches the kernel's barriers.
+// From then on every wait is short, the ones for copies still in flight and the
+// ones for rows that will not come (refill), so that the kernel ends within
+// seconds whatever the number of rows.
 __device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity) {
   if (tc::mbar_try_wait(bar, parity)) return;
   const unsigned long long t0 = tc::gtime();
   for (uint32_t i = 0; !tc::mbar_try_wait(bar, parity); ++i)
-    if ((i & 255u) == 255u && tc::gtime() - t0 > kRingWaitNs) {
-      flag_device_error(kDevTimeout);
+    if ((i & 255u) == 255u &&
+        tc::gtime() - t0 > (*(volatile int*)&g_device_status == kDevTimeout ? kRingLostNs : kRingWaitNs)) {
+      atomicExch(&g_device_status, kDevTimeout);
       return;
     }
 }
@@ -408,6 +412,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
   extern __shared__ __align__(128) unsigned char ring_mem[];
   __shared__ float2 buf[2][32];
   __shared__ __align__(8) uint64_t bars[(BLOCK ? 1 : kRowsPerCta) * kMaxRing];
+  __shared__ volatile int lost[BLOCK ? 1 : kRowsPerCta];  // by group: a copy has not landed
   const Group<TPR, SUB> gr(a.lpr);
   const int t = gr.t, tpr = gr.tpr, d = (int)a.d, S = a.ring;
   const T *x = (const T*)a.x, *r = (const T*)a.r;
@@ -416,6 +421,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
   const uint32_t mem = tc::smem_u32(ring_mem) + (uint32_t)gr.index * S * stage;
   uint64_t* bar = bars + gr.index * kMaxRing;
   if (gr.lane == 0) {
+    lost[gr.index] = 0;
     for (int i = 0; i < S; ++i) tc::mbar_init(&bar[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tc::fence_async_smem();
@@ -428,6 +434,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
                                      (r ? fill_bytes<T, ELEM>(r, a.ldr, d, rb, gr.rpw, n) : 0u));
     fill_region<T, SUB, ELEM>(mem + st * stage, x, a.ldx, d, rb, gr.rpw, n, &bar[st]);
     if (r) fill_region<T, SUB, ELEM>(mem + st * stage + region, r, a.ldr, d, rb, gr.rpw, n, &bar[st]);
+  };
+  // A stage takes the next row once the one before has landed.  After a loss none
+  // does: the barrier's turn is not over, and must not get a second arrival.
+  auto refill = [&](long long rb, int st, uint32_t phase) {
+    if (!tc::mbar_try_wait(&bar[st], phase)) lost[gr.index] = 1;
+    if (!lost[gr.index]) fill(rb, st);
   };
   const long long blocks = SUB ? (a.rows + gr.rpw - 1) / gr.rpw : a.rows;
   if (gr.lane == 0)
@@ -510,7 +522,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_fwd(const FwdArgs a) {
     // before the copy that refills their stage.
     if (!BLOCK) __syncwarp();
     const long long next = rb + (BLOCK ? S - 1 : S) * gr.step;
-    if (gr.lane == 0 && next < blocks && (!BLOCK || rb != gr.first)) fill(next, BLOCK ? before : st);
+    if (gr.lane == 0 && next < blocks && (!BLOCK || rb != gr.first))
+      refill(next, BLOCK ? before : st, BLOCK && st == 0 ? ph ^ 1u : ph);
     before = st;
     if (++st == S) { st = 0; ph ^= 1u; }
     const f32x2 nmu = pair(-mu, -mu);
@@ -632,6 +645,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
   extern __shared__ __align__(128) unsigned char ring_mem[];
   __shared__ float2 buf[2][32];
   __shared__ __align__(8) uint64_t bars[(BLOCK ? 1 : kRowsPerCta) * kMaxRing];
+  __shared__ volatile int lost[BLOCK ? 1 : kRowsPerCta];  // by group: a copy has not landed
   const Group<TPR, SUB> gr(a.lpr);
   const int t = gr.t, tpr = gr.tpr, d = (int)a.d, S = a.ring;
   const T *x = (const T*)a.x, *dy = (const T*)a.dy, *dr = (const T*)a.dr;
@@ -640,6 +654,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
   const uint32_t mem = tc::smem_u32(ring_mem) + (uint32_t)gr.index * S * stage;
   uint64_t* bar = bars + gr.index * kMaxRing;
   if (gr.lane == 0) {
+    lost[gr.index] = 0;
     for (int i = 0; i < S; ++i) tc::mbar_init(&bar[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tc::fence_async_smem();
@@ -654,6 +669,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
     fill_region<T, SUB, ELEM>(mem + st * stage, x, a.ldx, d, rb, gr.rpw, n, &bar[st]);
     fill_region<T, SUB, ELEM>(mem + st * stage + region, dy, a.lddy, d, rb, gr.rpw, n, &bar[st]);
     if (dr) fill_region<T, SUB, ELEM>(mem + st * stage + 2 * region, dr, a.lddr, d, rb, gr.rpw, n, &bar[st]);
+  };
+  // A stage takes the next row once the one before has landed.  After a loss none
+  // does: the barrier's turn is not over, and must not get a second arrival.
+  auto refill = [&](long long rb, int st, uint32_t phase) {
+    if (!tc::mbar_try_wait(&bar[st], phase)) lost[gr.index] = 1;
+    if (!lost[gr.index]) fill(rb, st);
   };
   const long long blocks = SUB ? (a.rows + gr.rpw - 1) / gr.rpw : a.rows;
   if (gr.lane == 0)
@@ -770,7 +791,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
     // past a CTA's barrier every thread is done with the row before this one
     if (BLOCK) {
       const long long next = rb + (S - 1) * gr.step;
-      if (gr.lane == 0 && next < blocks && rb != gr.first) fill(next, before);
+      if (gr.lane == 0 && next < blocks && rb != gr.first) refill(next, before, st == 0 ? ph ^ 1u : ph);
     }
     if (a.dx && on) {
       const RowFold f = fold_row(rs, s.x * inv_d, s.y * inv_d);
@@ -799,7 +820,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_ln_bwd(const BwdArgs a) {
     if (!BLOCK) {
       __syncwarp();
       const long long next = rb + S * gr.step;
-      if (gr.lane == 0 && next < blocks) fill(next, st);
+      if (gr.lane == 0 && next < blocks) refill(next, st, ph);
     }
     before = st;
     if (++st == S) { st = 0; ph ^= 1u; }
