@@ -152,6 +152,8 @@ def mat(t: torch.Tensor | None) -> AalMat:
     if rows > 0 and cols > 1 and t.stride(1) != 1:
         raise ValueError("tensor must be row-major (unit column stride)")
     ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if t.numel() > 0 and ld < cols:  # expanded rows: the library would read past them
+        raise ValueError("the rows of a tensor must not overlap")
     if t.numel() > 0 and not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
     return AalMat(t.data_ptr() if t.numel() > 0 else None, dt, rows, cols, max(ld, cols))

@@ -403,3 +403,19 @@ def test_the_marshaller_is_built_for_this_interpreter(lib):
     assert os.path.basename(build.FASTCALL) == "_fastcall" + suffix
     assert os.path.samefile(aal._fast().__file__, build.FASTCALL)
     assert not os.path.exists(os.path.join(build.PKG, "_fastcall.so"))
+
+
+def test_every_call_refuses_rows_that_overlap(lib):
+    """An expanded row is one row of memory: described as many, a kernel would
+    read past it.  (Host tensors: nothing launches.)"""
+    bf = torch.bfloat16
+    one, X = torch.empty(1, 8, dtype=bf).expand(4, 8), torch.empty(4, 8, dtype=bf)
+    for call in (lambda t: aal.mat(t), lambda t: aal.aal_square_product("Q", 2, t, X, X),
+                 lambda t: aal.aal_project_fwd("Q", 2, aal.row_rule(seq_len=4), t, X, X),
+                 lambda t: aal.aal_layer_norm_fwd(t, None, None, X)):
+        with pytest.raises(ValueError, match="overlap"):
+            call(one)
+        with pytest.raises(ValueError, match="overlap"):
+            call(torch.empty(40, dtype=bf).as_strided((4, 8), (3, 1)))
+    m = aal.mat(torch.empty(0, 8, dtype=bf))
+    assert (m.rows, m.cols, m.ld) == (0, 8, 8)
