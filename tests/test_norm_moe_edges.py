@@ -419,3 +419,51 @@ def test_every_call_refuses_rows_that_overlap(lib):
             call(torch.empty(40, dtype=bf).as_strided((4, 8), (3, 1)))
     m = aal.mat(torch.empty(0, 8, dtype=bf))
     assert (m.rows, m.cols, m.ld) == (0, 8, 8)
+
+
+# --------------------------------------------------------------- calls side by side
+@gpu
+def test_calls_of_several_threads_at_once(cuda):
+    """Four threads, a stream and tensors each, calling at the same time (the
+    binding lets them): every one gets what it gets alone."""
+    def work(seed):
+        gen = torch.Generator().manual_seed(seed)
+        shape = [(3, 768), (64, 2048), (5, 1003), (9, 8192)][seed % 4]
+        X, dY = (torch.randn(*shape, generator=gen).bfloat16().cuda() for _ in range(2))
+        Y, dX = torch.empty_like(X), torch.empty_like(X)
+        mean, rstd = torch.empty(shape[0], device="cuda"), torch.empty(shape[0], device="cuda")
+        dg = torch.empty(shape[1], device="cuda")
+        m = Moe(3 + 30 * seed, 16, 3, 96, 64, "Q", 2, "f32" if seed % 2 else "bf16", seed=seed)
+        ws = torch.empty(max(256, aal.aal_layer_norm_bwd_workspace_size(*shape)), dtype=torch.uint8, device="cuda")
+
+        def step():
+            aal.aal_set_workspace(ws)
+            aal.aal_layer_norm_fwd(X, None, None, Y, mean=mean, rstd=rstd)
+            aal.aal_layer_norm_bwd(X, None, mean, rstd, dY, dX=dX, dgamma=dg)
+            m.run()
+            aal.aal_set_workspace(None)
+            return [t.clone() for t in (Y, dX, dg, m.y, m.ids)]
+        return step
+
+    steps = [work(s) for s in range(4)]
+    want = [s() for s in steps]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(step, expect):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = step()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(g, e) for g, e in zip(got, expect)):
+                        wrong.append("differs")
+        except Exception as e:  # an assertion here would not reach the test
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(steps, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
