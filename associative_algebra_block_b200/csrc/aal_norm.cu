@@ -19,9 +19,9 @@
 // order, so results do not depend on timing.
 //
 // Measured, microseconds a call in a graph, against the bytes at the copy rate
-// of 6.53 TB/s:  forward 12288 x 768 bf16 with residual 16.0 (11.6), 2048 x
+// of 6.53 TB/s:  forward 12288 x 768 bf16 with residual 16.3 (11.6), 2048 x
 // 4096 fp32 17.0 (10.3), 4099 x 1003 bf16 10.1 (2.5);  backward 32768 x 5120
-// bf16 with dR 207 (205), 12288 x 768 22.5 (11.6), 2047 x 1001 fp32 17-18
+// bf16 with dR 208 (205), 12288 x 768 22.5 (11.6), 2047 x 1001 fp32 17-18
 // (3.8), 96 x 2048 7.4.  Large calls are bound by HBM; those of a few rows a
 // CTA by the ring's start, the reductions of the rows and, backward, the second
 // launch.
@@ -335,7 +335,7 @@ __device__ __forceinline__ void row_get(uint32_t row, int i, int tpr, int left, 
 }
 // A thread's vector i of a row less the row's mean.  bf16 elements are widened by
 // the addition itself, one mixed-precision instruction an element (32768 x 5120
-// backward 207 us; with a pair addition after the widening 217.5).
+// backward 208 us; with a pair addition after the widening 217).
 template <typename T, bool ELEM, int TPR>
 __device__ __forceinline__ void row_get_less(uint32_t row, int i, int tpr, int left, float mean,
                                              f32x2 (&v)[Vec<T>::pairs]) {
@@ -996,7 +996,7 @@ struct Plan {
 // of up to half a vector a lane (30000 x 64: 6.0 against 14.0 with a row a
 // warp, backward 9.4 against 18.3), a CTA one of 16 elements a thread.  A SM
 // holds up to 1024 threads of such CTAs forward (2048 x 4096 fp32: 17.0 us
-// against 20.5 with 512) and 640 backward (32768 x 5120: 209 against 290 with
+// against 20.5 with 512) and 640 backward (32768 x 5120: 208 against 290 with
 // 320; each CTA leaves a row of column sums).  ``arrays``: input arrays of a
 // stage (3 for the backward); pes: bytes of a gamma element.
 static Plan plan(long long d, int es, bool aligned, int arrays, int pes) {
